@@ -81,6 +81,16 @@ Where classify(const void* p, const void** dev) {
 
 bool is_device(const void* p) { return p != nullptr && classify(p, nullptr) == Where::kDevice; }
 
+bool is_here(const void* p) {
+    cudaPointerAttributes a;
+    int dev = 0;
+    if (p == nullptr || cudaPointerGetAttributes(&a, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == dev);
+}
+
 bool dims_ok(int Hkv, int d) { return Hkv >= 1 && d >= 32 && d <= kMaxD && d % 32 == 0; }
 
 bool heads_ok(int Hq, int Hkv) {
@@ -456,6 +466,156 @@ int fathom_decode_step(const fathom_store* store, const void* q, int q_dtype, co
                                    budget_bits, fixed_r, k, static_cast<const uint16_t*>(kd),
                                    static_cast<const uint16_t*>(vd), row_stride, rows_n, rows_host_resident, kv_groups,
                                    depths, idx, top_scores, out, workspace, (cudaStream_t)stream));
+}
+
+namespace {
+// Row arrays of the cache: alignment, stride and residency; resolved to device-usable addresses.
+int resolve_rows(const uint16_t* rows, int64_t row_stride, int d, int host, const uint16_t** dev) {
+    if (!rows || row_stride < d || row_stride % 8 || (reinterpret_cast<uintptr_t>(rows) & 15)) return FATHOM_EINVAL;
+    const void* p = nullptr;
+    if (classify(rows, &p) != (host ? Where::kHostPinned : Where::kDevice)) return FATHOM_EINVAL;
+    if (!host && !is_here(rows)) return FATHOM_EINVAL;
+    *dev = static_cast<const uint16_t*>(p);
+    return FATHOM_OK;
+}
+inline bool dtype_ok(int t) { return t == FATHOM_F32 || t == FATHOM_BF16; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+}  // namespace
+
+int fathom_qk_norm_rope(const void* qkv, int dtype, int64_t token_stride, int n_tokens, int n_q_heads, int n_kv_heads,
+                        int d, const void* q_weight, const void* k_weight, int w_dtype, float eps,
+                        const int32_t* positions, const float* inv_freq, int rot_dim, int interleaved, void* q_out,
+                        uint16_t* K_rows, uint16_t* V_rows, int64_t row_stride, int rows_host_resident, int64_t rows_n,
+                        int64_t row0, fathom_stream_t stream) {
+    if (!qkv || !q_out || !K_rows || !V_rows || n_tokens < 1 || !dims_ok(n_kv_heads, d) || n_q_heads < 1 ||
+        n_q_heads % n_kv_heads || n_q_heads > 65536)
+        return FATHOM_EINVAL;
+    if (!dtype_ok(dtype) || ((q_weight || k_weight) && !dtype_ok(w_dtype)) || !q_weight != !k_weight)
+        return FATHOM_EINVAL;
+    if (rot_dim < 0 || rot_dim > d || rot_dim % 16 || (rot_dim > 0 && !inv_freq) || !(eps >= 0.0f)) return FATHOM_EINVAL;
+    const int64_t per16 = dtype == FATHOM_BF16 ? 8 : 4;
+    if (token_stride < (int64_t)(n_q_heads + 2 * n_kv_heads) * d || token_stride % per16) return FATHOM_EINVAL;
+    if (row0 < 0 || rows_n < n_tokens || row0 > rows_n - n_tokens || (!positions && row0 + n_tokens - 1 > INT32_MAX))
+        return FATHOM_EINVAL;
+    if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(q_weight) || !aligned16(k_weight)) return FATHOM_EINVAL;
+    const uint16_t *kr, *vr;
+    int rc = resolve_rows(K_rows, row_stride, d, rows_host_resident, &kr);
+    if (!rc) rc = resolve_rows(V_rows, row_stride, d, rows_host_resident, &vr);
+    if (rc) return rc;
+    if (!is_here(qkv) || !is_here(q_out) || (q_weight && (!is_here(q_weight) || !is_here(k_weight))) ||
+        (positions && !is_here(positions)) || (rot_dim > 0 && !is_here(inv_freq)))
+        return FATHOM_EINVAL;
+    return to_status(launch_rope(qkv, dtype, token_stride, n_tokens, n_q_heads, n_kv_heads, d, q_weight, k_weight,
+                                 w_dtype, eps, positions, inv_freq, rot_dim, interleaved, q_out,
+                                 const_cast<uint16_t*>(kr), const_cast<uint16_t*>(vr), row_stride, rows_n, row0,
+                                 (cudaStream_t)stream));
+}
+
+namespace {
+// A store that may be empty (n = 0) or about to grow to n_new keys.
+int resolve_growing(const fathom_store* s, int64_t n_new, const uint32_t** planes, const uint16_t** scales) {
+    if (!s || s->n < 0 || n_new < 1) return FATHOM_EINVAL;
+    fathom_store t = *s;
+    t.n = n_new;
+    const int rc = resolve_store(&t, planes, scales);
+    if (rc) return rc;
+    if (!s->host_resident && (!is_here(s->planes) || !is_here(s->scales))) return FATHOM_EINVAL;
+    return FATHOM_OK;
+}
+}  // namespace
+
+int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows, const uint16_t* V_rows,
+                       int64_t row_stride, int rows_host_resident, int64_t rows_n, int64_t n_new,
+                       fathom_stream_t stream) {
+    const uint32_t *kp, *vp = nullptr;
+    const uint16_t *ksc, *vsc = nullptr, *kr, *vr = nullptr;
+    int rc = resolve_growing(K, n_new, &kp, &ksc);
+    if (rc) return rc;
+    if (n_new <= K->n || rows_n < n_new || K == V || !V != !V_rows) return FATHOM_EINVAL;
+    rc = resolve_rows(K_rows, row_stride, K->d, rows_host_resident, &kr);
+    if (rc) return rc;
+    if (V) {
+        if (V->n != K->n || V->n_kv_heads != K->n_kv_heads || V->d != K->d || V->planes == K->planes)
+            return FATHOM_EINVAL;
+        rc = resolve_growing(V, n_new, &vp, &vsc);
+        if (!rc) rc = resolve_rows(V_rows, row_stride, K->d, rows_host_resident, &vr);
+        if (rc) return rc;
+    }
+    if (K->n_kv_heads > 32767) return FATHOM_EUNSUPPORTED;   // heads of both stores along the grid's y
+    cudaError_t e = launch_append_rows(kr, const_cast<uint32_t*>(kp), const_cast<uint16_t*>(ksc), K->n_pad, vr,
+                                       const_cast<uint32_t*>(vp), const_cast<uint16_t*>(vsc), V ? V->n_pad : 0,
+                                       K->n_kv_heads, K->d, rows_n, row_stride, K->n / kBlock, n_new,
+                                       (cudaStream_t)stream);
+    if (e != cudaSuccess) return FATHOM_ECUDA;
+    K->n = n_new;
+    if (V) V->n = n_new;
+    return FATHOM_OK;
+}
+
+size_t fathom_store_attend_workspace_bytes(int n_sessions, int n_tokens, int n_q_heads, int n_kv_heads, int d) {
+    if (n_sessions < 1 || n_sessions > kMaxSets || n_tokens < 1 || n_tokens > kMaxAttendTokens ||
+        !dims_ok(n_kv_heads, d) || !heads_ok(n_q_heads, n_kv_heads) || n_q_heads > 65536)
+        return 0;
+    return store_attend_workspace_bytes(n_sessions, n_tokens, n_q_heads, n_kv_heads, d);
+}
+
+namespace {
+// visible: per session, or null (causal: a token sees its own past; else every key)
+int store_attend(const fathom_store* Ks, const fathom_store* Vs, int S, const void* q, int q_dtype, int T, int Hq,
+                 const int64_t* visible, int causal, float* out, float* parts, void* ws, size_t ws_bytes,
+                 fathom_stream_t stream) {
+    float* dst = parts ? parts : out;
+    if (!Ks || !Vs || S < 1 || S > kMaxSets || !q || !dst || !ws || T < 1 || T > kMaxAttendTokens)
+        return FATHOM_EINVAL;
+    if (!dtype_ok(q_dtype) || Hq > 65536) return FATHOM_EINVAL;
+    const int Hkv = Ks[0].n_kv_heads, d = Ks[0].d;
+    if (!dims_ok(Hkv, d) || !heads_ok(Hq, Hkv)) return FATHOM_EINVAL;
+    if (d != 32 && d != 64 && d != 128 && d != 256) return FATHOM_EUNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(ws) & 255) return FATHOM_EINVAL;
+    if (ws_bytes < store_attend_workspace_bytes(S, T, Hq, Hkv, d)) return FATHOM_ENOMEM;
+    AttendMap m;
+    m.nsess = S;
+    for (int s = 0; s < S; ++s) {
+        const fathom_store &k = Ks[s], &v = Vs[s];
+        if (k.n_kv_heads != Hkv || v.n_kv_heads != Hkv || k.d != d || v.d != d || k.n != v.n || k.n > INT32_MAX)
+            return FATHOM_EINVAL;
+        // an empty store needs no arrays' contents, but is checked like any other
+        int rc = resolve_growing(&k, k.n > 0 ? k.n : 1, &m.k_planes[s], &m.k_scales[s]);
+        if (!rc) rc = resolve_growing(&v, v.n > 0 ? v.n : 1, &m.v_planes[s], &m.v_scales[s]);
+        if (rc) return rc;
+        m.k_pad[s] = k.n_pad;
+        m.v_pad[s] = v.n_pad;
+        m.n[s] = k.n;
+        int64_t vis = visible ? visible[s] : (causal ? k.n - T + 1 : k.n);
+        if (vis > k.n) vis = k.n;
+        if (vis < -T) vis = -T;   // no token sees a key
+        m.visible[s] = vis;
+    }
+    if (!is_here(q) || !is_here(dst) || !is_here(ws)) return FATHOM_EINVAL;
+    return to_status(launch_store_attend(m, Hkv, d, q, q_dtype, T, Hq, out, parts, ws, (cudaStream_t)stream));
+}
+}  // namespace
+
+int fathom_store_attend(const fathom_store* K, const fathom_store* V, const void* q, int q_dtype, int n_tokens,
+                        int n_q_heads, int causal, float* out, void* workspace, size_t workspace_bytes,
+                        fathom_stream_t stream) {
+    return store_attend(K, V, 1, q, q_dtype, n_tokens, n_q_heads, nullptr, causal, out, nullptr, workspace,
+                        workspace_bytes, stream);
+}
+
+int fathom_store_attend_partial(const fathom_store* K, const fathom_store* V, const void* q, int q_dtype, int n_tokens,
+                                int n_q_heads, int64_t visible, float* parts, void* workspace, size_t workspace_bytes,
+                                fathom_stream_t stream) {
+    if (!parts) return FATHOM_EINVAL;
+    return store_attend(K, V, 1, q, q_dtype, n_tokens, n_q_heads, &visible, 0, nullptr, parts, workspace,
+                        workspace_bytes, stream);
+}
+
+int fathom_store_attend_batched(const fathom_store* K, const fathom_store* V, int n_sessions, const void* q,
+                                int q_dtype, int n_tokens, int n_q_heads, int causal, float* out, void* workspace,
+                                size_t workspace_bytes, fathom_stream_t stream) {
+    return store_attend(K, V, n_sessions, q, q_dtype, n_tokens, n_q_heads, nullptr, causal, out, nullptr, workspace,
+                        workspace_bytes, stream);
 }
 
 int fathom_last_device_status(fathom_stream_t stream) {

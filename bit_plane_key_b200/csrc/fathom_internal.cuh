@@ -14,6 +14,7 @@ constexpr int kBlock = 64;     // tokens per shared block scale
 constexpr int kPad = 1024;     // key padding granule of the store: plane rows start 128-byte aligned
 constexpr int kMaxD = 256;     // largest supported head dimension
 constexpr int kMaxTopK = 4096; // largest supported k
+constexpr int kMaxAttendTokens = 4096; // largest query token count of an attention over stores
 constexpr size_t kMaxSmem = 227 * 1024;  // opt-in shared memory per CTA on sm_100
 
 __host__ __device__ inline int64_t n_pad_of(int64_t n) { return ((n + kPad - 1) / kPad) * kPad; }
@@ -87,6 +88,8 @@ cudaError_t launch_ex(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem
 enum class Where { kDevice, kHostPinned, kOther };
 Where classify(const void* p, const void** dev);
 bool is_device(const void* p);
+// device memory of the current device
+bool is_here(const void* p);
 bool dims_ok(int Hkv, int d);
 bool heads_ok(int Hq, int Hkv);
 bool scan_fits(int d, int Hq, int Hkv);
@@ -187,6 +190,38 @@ cudaError_t launch_attend(const void* q, int q_dtype, const uint16_t* K_rows, co
                           int64_t row_stride, const int32_t* idx, int Hq, int Hkv, int64_t n, int d, int k, int sort_rows, float* out,
                           cudaStream_t stream, int64_t key0 = 0, float* parts = nullptr, bool pdl = false);
 cudaError_t launch_attend_merge(const float* parts, int world, int Hq, int d, float* out, cudaStream_t stream);
+
+// Norms, rotation and the writes into the row cache (rope.cu).
+cudaError_t launch_rope(const void* qkv, int dtype, int64_t token_stride, int n_tokens, int Hq, int Hkv, int d,
+                        const void* q_weight, const void* k_weight, int w_dtype, float eps, const int32_t* positions,
+                        const float* inv_freq, int rot, int interleaved, void* q_out, uint16_t* K_rows,
+                        uint16_t* V_rows, int64_t row_stride, int64_t rows_n, int64_t row0, cudaStream_t stream);
+// Packs blocks [blk0, ceil(n/64)) of the K store, and of the V store unless
+// V_rows is null, from the row cache (append.cu).
+cudaError_t launch_append_rows(const uint16_t* K_rows, uint32_t* k_planes, uint16_t* k_scales, int64_t k_pad,
+                               const uint16_t* V_rows, uint32_t* v_planes, uint16_t* v_scales, int64_t v_pad, int Hkv,
+                               int d, int64_t rows_n, int64_t row_stride, int64_t blk0, int64_t n, cudaStream_t stream);
+
+// Sessions of an attention over stores: query token t of session s sees the
+// keys below min(n[s], visible[s] + t).  launch_store_attend fills tiles (per
+// row of session s) and unit0 (prefix sums over the sessions' rows).
+struct AttendMap {
+    int nsess;
+    const uint32_t* k_planes[kMaxSets];
+    const uint16_t* k_scales[kMaxSets];
+    const uint32_t* v_planes[kMaxSets];
+    const uint16_t* v_scales[kMaxSets];
+    int64_t k_pad[kMaxSets];
+    int64_t v_pad[kMaxSets];
+    int64_t n[kMaxSets];
+    int64_t visible[kMaxSets];
+    int tiles[kMaxSets];
+    int64_t unit0[kMaxSets + 1];
+};
+size_t store_attend_workspace_bytes(int S, int T, int Hq, int Hkv, int d);
+// parts non-null: per-row partials [S][T][Hq][d + 2] instead of out
+cudaError_t launch_store_attend(AttendMap& map, int Hkv, int d, const void* q, int q_dtype, int T, int Hq, float* out,
+                                float* parts, void* ws, cudaStream_t stream);
 
 cudaError_t launch_probe(const void* src, size_t bytes, unsigned long long* sink, int ctas,
                          cudaStream_t stream);

@@ -1,0 +1,189 @@
+// Norms of query and key heads with the rotation by position, in one pass
+// over the rows of a layer's fused projection, written where the decode path
+// reads them: queries to their own array, keys (rotated) and values (as they
+// are) to the layer's row cache.
+//
+//   y = x / sqrt(mean_c x_c^2 + eps) * w               (heads with a weight)
+//   (a, b) <- (a cos f - b sin f, b cos f + a sin f)    for the pairs (a, b) of
+//   the first rot_dim channels, f = position * inv_freq[pair]
+//
+// in fp32, rounded once to the output type.  The angle is reduced in fp64 (at
+// position 10^6 an fp32 product has lost 0.03 rad): r = 4 f / 2 pi less its
+// nearest integer k lies in [-1/2, 1/2], so rounding r to fp32 costs at most
+// 2^-26 * pi / 2 = 2.3e-8 rad, less than the rounding of the sine itself.
+//
+// One CTA per token and set of heads: the token's sines and cosines are
+// computed once into shared memory, then groups of lanes take a head each.
+// A lane holds 16 channels of its head as two 8-channel pieces; for pairs
+// (i, i + rot_dim / 2) the two pieces are the two sides of the same 8 pairs,
+// so the rotation needs no exchange between lanes.
+#include "fathom_internal.cuh"
+
+namespace fathom {
+namespace {
+
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ void load8(const void* p, int dtype, int64_t i, float* x) {
+    if (dtype == FATHOM_BF16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    } else {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4 a = f[0], b = f[1];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+}
+
+__device__ __forceinline__ void store8(void* p, int dtype, int64_t i, const float* x) {
+    if (dtype == FATHOM_BF16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        f[0] = make_float4(x[0], x[1], x[2], x[3]);
+        f[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// sin and cos of position * inv_freq
+__device__ __forceinline__ float2 sin_cos(int position, float inv_freq) {
+    const double quarter = (double)position * (double)inv_freq * 0.63661977236758134308;   // 2 / pi
+    const double k = rint(quarter);
+    const float r = (float)(quarter - k);
+    float s, c;
+    sincospif(0.5f * r, &s, &c);
+    const int q = (int)((long long)k & 3);
+    const float s1 = (q & 1) ? c : s, c1 = (q & 1) ? s : c;
+    return make_float2((q & 2) ? -s1 : s1, (q == 1 || q == 2) ? -c1 : c1);
+}
+
+// LPR = lanes per head: d/16 rounded up to a power of two
+template <int LPR>
+__global__ void __launch_bounds__(kThreads)
+rope_kernel(const void* __restrict__ qkv, int dtype, int64_t token_stride, int Hq, int Hkv, int d,
+            const void* __restrict__ q_weight, const void* __restrict__ k_weight, int w_dtype, float eps,
+            const int32_t* __restrict__ positions, const float* __restrict__ inv_freq, int rot, int interleaved,
+            void* __restrict__ q_out, uint16_t* __restrict__ K_rows, uint16_t* __restrict__ V_rows, int64_t row_stride,
+            int64_t rows_n, int64_t row0) {
+    __shared__ float2 s_sc[kMaxD / 2];   // (sin, cos) of the token's pairs
+    const int64_t t = blockIdx.x;
+    const int H = Hq + 2 * Hkv;
+    const int position = positions ? positions[t] : (int)(row0 + t);
+    for (int i = threadIdx.x; i < rot / 2; i += kThreads) s_sc[i] = sin_cos(position, inv_freq[i]);
+    __syncthreads();
+
+    const int j = threadIdx.x % LPR;
+    const bool on = j < d / 16;
+    // the lane's two pieces: of a rotated head the two sides of 8 pairs, then the channels behind
+    const int rl = rot / 16;   // lanes that hold rotated channels
+    int c0, c1;
+    if (interleaved || j >= rl) {
+        c0 = 16 * j;
+        c1 = c0 + 8;
+    } else {
+        c0 = 8 * j;
+        c1 = rot / 2 + 8 * j;
+    }
+    const int per_cta = kThreads / LPR;
+    for (int h0 = blockIdx.y * per_cta; h0 < H; h0 += gridDim.y * per_cta) {
+        const int h = h0 + threadIdx.x / LPR;
+        const bool act = on && h < H;
+        float a[8], b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = b[e] = 0.0f;
+        if (act) {
+            const int64_t base = t * token_stride + (int64_t)h * d;
+            load8(qkv, dtype, base + c0, a);
+            load8(qkv, dtype, base + c1, b);
+        }
+        const void* w = h < Hq ? q_weight : k_weight;
+        if (w) {   // the same for every head of the call: all lanes take part in the sums
+            float ss = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (act && h < Hq + Hkv) {
+                const float r = 1.0f / sqrtf(ss / (float)d + eps);
+                float wa[8], wb[8];
+                load8(w, w_dtype, c0, wa);
+                load8(w, w_dtype, c1, wb);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    a[e] *= r * wa[e];
+                    b[e] *= r * wb[e];
+                }
+            }
+        }
+        if (!act) continue;
+        if (h < Hq + Hkv && j < rl) {
+            if (interleaved) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 fa = s_sc[8 * j + e / 2], fb = s_sc[8 * j + 4 + e / 2];
+                    const float a0 = a[e], b0 = b[e];
+                    a[e] = a0 * fa.y - a[e + 1] * fa.x;
+                    a[e + 1] = a[e + 1] * fa.y + a0 * fa.x;
+                    b[e] = b0 * fb.y - b[e + 1] * fb.x;
+                    b[e + 1] = b[e + 1] * fb.y + b0 * fb.x;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = s_sc[8 * j + e];
+                    const float a0 = a[e];
+                    a[e] = a0 * f.y - b[e] * f.x;
+                    b[e] = b[e] * f.y + a0 * f.x;
+                }
+            }
+        }
+        if (h < Hq) {
+            const int64_t base = (t * Hq + h) * d;
+            store8(q_out, dtype, base + c0, a);
+            store8(q_out, dtype, base + c1, b);
+        } else {
+            const bool key = h < Hq + Hkv;
+            const int g = key ? h - Hq : h - Hq - Hkv;
+            const int64_t base = ((int64_t)g * rows_n + row0 + t) * row_stride;
+            store8(key ? K_rows : V_rows, FATHOM_BF16, base + c0, a);
+            store8(key ? K_rows : V_rows, FATHOM_BF16, base + c1, b);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const void* qkv, int dtype, int64_t token_stride, int n_tokens, int Hq, int Hkv, int d,
+                        const void* q_weight, const void* k_weight, int w_dtype, float eps, const int32_t* positions,
+                        const float* inv_freq, int rot, int interleaved, void* q_out, uint16_t* K_rows,
+                        uint16_t* V_rows, int64_t row_stride, int64_t rows_n, int64_t row0, cudaStream_t stream) {
+    auto go = [&](auto kern, int lpr) {
+        const int per_cta = kThreads / lpr, sets = (Hq + 2 * Hkv + per_cta - 1) / per_cta;
+        // many tokens: a CTA takes all heads of its token and computes the sines
+        // once; few tokens: the heads spread over CTAs
+        const int want = (1184 + n_tokens - 1) / n_tokens;
+        dim3 grid((unsigned)n_tokens, (unsigned)(want < sets ? want : sets));
+        kern<<<grid, kThreads, 0, stream>>>(qkv, dtype, token_stride, Hq, Hkv, d, q_weight, k_weight, w_dtype, eps,
+                                            positions, inv_freq, rot, interleaved, q_out, K_rows, V_rows, row_stride,
+                                            rows_n, row0);
+        return cudaGetLastError();
+    };
+    if (d <= 32) return go(rope_kernel<2>, 2);
+    if (d <= 64) return go(rope_kernel<4>, 4);
+    if (d <= 128) return go(rope_kernel<8>, 8);
+    return go(rope_kernel<16>, 16);
+}
+
+}  // namespace fathom

@@ -74,6 +74,14 @@ _sig("fathom_scan_topk_batched", _I, [_SP, _I, _P, _I, _P, _I, _I, _P, _P, _P, _
 _sig("fathom_scan_topk_noalloc", _I, [_SP, _P, _I, _P, _I, _I, _P, _P, _P])
 _sig("fathom_decode_workspace_bytes", _Z, [_SP, _I, _I, _I])
 _sig("fathom_decode_step", _I, [_SP, _P, _I, _P, _I, _I, _I, _I, _P, _P, _L, _L, _I, _I, _P, _P, _P, _P, _P, _Z, _P])
+_F = ctypes.c_float
+_sig("fathom_qk_norm_rope", _I, [_P, _I, _L, _I, _I, _I, _I, _P, _P, _I, _F, _P, _P, _I, _I, _P, _P, _P, _L, _I, _L, _L,
+                                 _P])
+_sig("fathom_append_rows", _I, [_SP, _SP, _P, _P, _L, _I, _L, _L, _P])
+_sig("fathom_store_attend_workspace_bytes", _Z, [_I, _I, _I, _I, _I])
+_sig("fathom_store_attend", _I, [_SP, _SP, _P, _I, _I, _I, _I, _P, _P, _Z, _P])
+_sig("fathom_store_attend_partial", _I, [_SP, _SP, _P, _I, _I, _I, _L, _P, _P, _Z, _P])
+_sig("fathom_store_attend_batched", _I, [_SP, _SP, _I, _P, _I, _I, _I, _I, _P, _P, _Z, _P])
 
 
 def lib():
@@ -411,3 +419,131 @@ def decode_step(store, q, sigma2, budget_bits, k, K_rows, V_rows, fixed_r=0, kv_
                                    _ptr(top_scores), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
            "fathom_decode_step")
     return depths, idx, top_scores, out
+
+
+def _check_rows(K_rows, V_rows):
+    """Strides of a row cache, K_rows and V_rows [Hkv][rows][d]; returns (row stride, rows, host-resident)."""
+    rows_n = K_rows.shape[1]
+    if K_rows.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or V_rows.dtype != K_rows.dtype:
+        raise TypeError("K_rows and V_rows hold bfloat16")
+    if (K_rows.shape != V_rows.shape or K_rows.stride() != V_rows.stride() or K_rows.stride(2) != 1
+            or (K_rows.shape[0] > 1 and K_rows.stride(0) != rows_n * K_rows.stride(1))
+            or K_rows.is_cuda != V_rows.is_cuda):
+        raise ValueError("K_rows and V_rows need strides (rows*s, s, 1), the same for both")
+    return int(K_rows.stride(1)), int(rows_n), int(not K_rows.is_cuda)
+
+
+def _check_out(t, shape, dtype, what):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s %s" % (what, dtype, tuple(shape)))
+
+
+def qk_norm_rope(qkv, n_q_heads, n_kv_heads, inv_freq, K_rows, V_rows, row0, q_weight=None, k_weight=None, eps=1e-6,
+                 positions=None, interleaved=False, out=None, stream=None):
+    """Norms (when weights are given) and rotation of a projection's query and
+    key heads: qkv [T][Hq + 2 Hkv][d] (float32 or bfloat16, a token's heads
+    contiguous), inv_freq f32 [rot_dim / 2].  Returns the queries [T][Hq][d] and
+    writes token t's key and value rows at row0 + t of the row cache (bf16 views
+    as sparse_attend).  positions i32 [T], default row0 + t."""
+    T, H, d = qkv.shape
+    if H != n_q_heads + 2 * n_kv_heads or qkv.stride(2) != 1 or (H > 1 and qkv.stride(1) != d):
+        raise ValueError("qkv must be [T][Hq + 2 Hkv][d] with a token's heads contiguous")
+    stride, rows_n, host = _check_rows(K_rows, V_rows)
+    if K_rows.shape[0] != n_kv_heads or K_rows.shape[2] != d:
+        raise ValueError("K_rows and V_rows must be [Hkv][rows][d]")
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _check_out(inv_freq, (rot // 2,), torch.float32, "inv_freq")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.numel() != d or not w.is_contiguous() or w.dtype != q_weight.dtype):
+            raise ValueError("q_weight and k_weight must be contiguous [d] of one dtype")
+    if positions is not None:
+        _check_out(positions, (T,), torch.int32, "positions")
+    if out is None:
+        out = torch.empty((T, n_q_heads, d), dtype=qkv.dtype, device=qkv.device)
+    _check_out(out, (T, n_q_heads, d), qkv.dtype, "out")
+    if T == 0:
+        return out
+    # a single token has no stride of its own
+    ts = int(qkv.stride(0)) if T > 1 else H * d
+    _check(_lib.fathom_qk_norm_rope(_ptr(qkv), _dtype_code(qkv), ts, T, int(n_q_heads), int(n_kv_heads), d,
+                                    _ptr(q_weight), _ptr(k_weight),
+                                    _dtype_code(q_weight) if q_weight is not None else F32, float(eps),
+                                    _ptr(positions), _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(out),
+                                    _ptr(K_rows), _ptr(V_rows), stride, host, rows_n, int(row0), _stream(stream)),
+           "fathom_qk_norm_rope")
+    return out
+
+
+def append_rows(k_store, v_store, K_rows, V_rows, n_new, stream=None):
+    """Grows the K store and the V store to n_new keys from the row cache (views
+    as sparse_attend, key i of the store = row i); v_store and V_rows None: the K
+    store alone."""
+    if (v_store is None) != (V_rows is None):
+        raise ValueError("v_store and V_rows go together")
+    stride, rows_n, host = _check_rows(K_rows, K_rows if V_rows is None else V_rows)
+    if K_rows.shape[0] != k_store.n_kv_heads or K_rows.shape[2] != k_store.d:
+        raise ValueError("K_rows must be [Hkv][rows][d] of the store")
+    _check(_lib.fathom_append_rows(k_store.c, v_store.c if v_store is not None else None, _ptr(K_rows), _ptr(V_rows),
+                                   stride, host, rows_n, int(n_new), _stream(stream)), "fathom_append_rows")
+    for st in (k_store, v_store):
+        if st is not None:
+            st.n = int(st._c.n)
+    return k_store, v_store
+
+
+def store_attend_workspace_bytes(store, n_sessions, n_tokens, n_q_heads):
+    return int(_lib.fathom_store_attend_workspace_bytes(int(n_sessions), int(n_tokens), int(n_q_heads),
+                                                        store.n_kv_heads, store.d))
+
+
+def _attend_args(store, q, lead, out, width, workspace):
+    """Checks q [lead...][Hq][d] and makes out f32 [lead...][Hq][width] and the workspace."""
+    if q.dim() != lead + 2 or q.shape[-1] != store.d or not q.is_contiguous():
+        raise ValueError("q must be contiguous with %d dimensions, the last of size %d" % (lead + 2, store.d))
+    shape = tuple(q.shape[:-1]) + (width,)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    _check_out(out, shape, torch.float32, "out")
+    S = q.shape[0] if lead == 2 else 1
+    T = q.shape[lead - 1] if lead else 1
+    if workspace is None:
+        nb = store_attend_workspace_bytes(store, S, T, q.shape[-2])
+        workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=q.device)
+    return out, T, workspace
+
+
+def store_attend(k_store, v_store, q, causal=True, out=None, workspace=None, stream=None):
+    """Attention over every key of the K store and the 4-bit values of the V
+    store: q [Hq][d] or [T][Hq][d] -> f32 of the same shape.  causal: the stores'
+    last T keys are the T tokens' own, each sees its past and itself; else every
+    token sees all keys."""
+    out, T, workspace = _attend_args(k_store, q, q.dim() - 2, out, k_store.d, workspace)
+    _check(_lib.fathom_store_attend(k_store.c, v_store.c, _ptr(q), _dtype_code(q), T, q.shape[-2], int(bool(causal)),
+                                    _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
+           "fathom_store_attend")
+    return out
+
+
+def store_attend_partial(k_store, v_store, q, visible, parts=None, workspace=None, stream=None):
+    """Partials f32 [..][Hq][d + 2] (as sparse_attend_partial) of attention over
+    this range's keys; token t sees those below visible + t."""
+    parts, T, workspace = _attend_args(k_store, q, q.dim() - 2, parts, k_store.d + 2, workspace)
+    _check(_lib.fathom_store_attend_partial(k_store.c, v_store.c, _ptr(q), _dtype_code(q), T, q.shape[-2],
+                                            int(visible), _ptr(parts), _ptr(workspace), workspace.numel(),
+                                            _stream(stream)), "fathom_store_attend_partial")
+    return parts
+
+
+def store_attend_batched(k_stores, v_stores, q, causal=True, out=None, workspace=None, stream=None):
+    """store_attend of the sessions (k_stores[s], v_stores[s]) in one pass: q
+    [S][T][Hq][d] -> f32 of the same shape."""
+    if len(k_stores) != q.shape[0] or len(v_stores) != q.shape[0]:
+        raise ValueError("one K store and one V store for each session of q")
+    out, T, workspace = _attend_args(k_stores[0], q, 2, out, k_stores[0].d, workspace)
+    _check(_lib.fathom_store_attend_batched(_store_array(k_stores), _store_array(v_stores), len(k_stores), _ptr(q),
+                                            _dtype_code(q), T, q.shape[-2], int(bool(causal)), _ptr(out),
+                                            _ptr(workspace), workspace.numel(), _stream(stream)),
+           "fathom_store_attend_batched")
+    return out

@@ -409,6 +409,106 @@ int fathom_decode_step(const fathom_store* store, const void* q, int q_dtype, co
                        fathom_stream_t stream);
 
 /*
+ * Norms of query and key heads with the rotation by position, from a layer's
+ * fused projection to where the decode path reads: the queries to q_out, keys
+ * and values to the layer's row cache (not on the pages, which start from
+ * finished queries and keys).  For each token and each query or key head, in
+ * fp32, rounded once:
+ *   y = x / sqrt(mean_c x_c^2 + eps) * weight      (with weights)
+ *   (a, b) <- (a cos f - b sin f, b cos f + a sin f), f = position * inv_freq[i],
+ *   for the pairs i of the first rot_dim channels: (i, i + rot_dim/2), or
+ *   (2i, 2i+1) when interleaved.  The angle is reduced in fp64.
+ * Value heads are copied.
+ *   qkv       device, token t's heads at element t * token_stride: Hq query heads,
+ *             Hkv key heads, Hkv value heads, d elements each; dtype FATHOM_F32 or
+ *             FATHOM_BF16; token_stride * element size a multiple of 16.
+ *   q_weight, k_weight  device, [d], w_dtype FATHOM_F32 or FATHOM_BF16; both NULL: no norm.
+ *   positions device, i32 [n_tokens], or NULL: token t is at position row0 + t.
+ *   inv_freq  device, f32 [rot_dim/2]; rot_dim a multiple of 16, at most d (0: no
+ *             rotation, inv_freq may be NULL).
+ *   q_out     device, [n_tokens][Hq][d], dtype as qkv.
+ *   K_rows, V_rows, row_stride, rows_host_resident  as fathom_sparse_attend; rows_n
+ *             rows per KV head; token t's rows are written at row0 + t of each KV
+ *             head, no other row is touched.
+ *   qkv, q_out, weights 16-byte aligned.  q_out and the rows must not overlap qkv.
+ * Errors: EINVAL for null pointers, bad sizes, strides, alignment or
+ * residency, one weight without the other, rows outside [0, rows_n).
+ */
+int fathom_qk_norm_rope(const void* qkv, int dtype, int64_t token_stride, int n_tokens, int n_q_heads, int n_kv_heads,
+                        int d, const void* q_weight, const void* k_weight, int w_dtype, float eps,
+                        const int32_t* positions, const float* inv_freq, int rot_dim, int interleaved, void* q_out,
+                        uint16_t* K_rows, uint16_t* V_rows, int64_t row_stride, int rows_host_resident, int64_t rows_n,
+                        int64_t row0, fathom_stream_t stream);
+
+/*
+ * Grows the K store and the V store of a layer from its row cache to n_new
+ * keys: fathom_append_keys for both, reading the rows where they lie.  A V
+ * store is a fathom_store packed from values.  The keys from the first of the
+ * last partial 64-token block on are read again from the rows.
+ *   K, V      stores with capacity for n_new keys and the same n, Hkv, d; V and
+ *             V_rows both NULL: the K store alone.  On success n becomes n_new.
+ *   K_rows, V_rows, row_stride, rows_host_resident, rows_n (>= n_new)  as
+ *             fathom_decode_step: key i of the store is row i.
+ * The result equals fathom_append_keys of the same rows, bit for bit.  Rows hold
+ * finite values.
+ * Errors: EINVAL for null pointers, n_new <= n, missing capacity, stores that
+ * differ or share planes, arrays not where the flags say or misaligned.
+ */
+int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows, const uint16_t* V_rows,
+                       int64_t row_stride, int rows_host_resident, int64_t rows_n, int64_t n_new,
+                       fathom_stream_t stream);
+
+/*
+ * Attention over the 4-bit stores themselves: every key, at all four planes,
+ * and 4-bit values (not on the pages, which attend over selected bf16 rows;
+ * for layers that read their whole context, short contexts, the checking of
+ * drafted tokens).
+ *   out[t][h] = softmax_i(q[t][h] . K_i / sqrt(d)) V_i over the keys i that token t
+ *   sees, K_ic = Delta_c (code_ic - 7.5) in the block scale Delta, V likewise,
+ *   fp32 accumulation; 0 for a token that sees no key.
+ * causal != 0: the stores' last n_tokens keys are the tokens' own, token t sees
+ * the keys below n - n_tokens + 1 + t.  causal == 0: every token sees all n keys.
+ *   K, V      stores with the same n, Hkv, d, n <= 2^31 - 1; each device- or
+ *             host-resident; n may be 0.
+ *   q         device, [n_tokens][Hq][d], FATHOM_F32 or FATHOM_BF16, finite values;
+ *             1 <= n_tokens <= 4096 (made for few tokens: the stores are read again
+ *             for every 16 (token, head of a group) pairs).
+ *   out       device, f32 [n_tokens][Hq][d].
+ *   workspace device, 256-byte aligned, fathom_store_attend_workspace_bytes() bytes;
+ *             contents need not be initialised, and are free once the call's
+ *             kernels are done.  Calls that overlap on the GPU need one each.
+ * A call with the same arguments gives the same bits.
+ * Errors: EINVAL for null pointers, bad sizes, stores that differ, arrays not on
+ * this device or not where host_resident says; ENOMEM for a short workspace;
+ * EUNSUPPORTED for d other than 32, 64, 128, 256.
+ */
+size_t fathom_store_attend_workspace_bytes(int n_sessions, int n_tokens, int n_q_heads, int n_kv_heads, int d);
+int fathom_store_attend(const fathom_store* K, const fathom_store* V, const void* q, int q_dtype, int n_tokens,
+                        int n_q_heads, int causal, float* out, void* workspace, size_t workspace_bytes,
+                        fathom_stream_t stream);
+
+/*
+ * fathom_store_attend over a key range split across GPUs: the partials of this
+ * range's keys, for fathom_attend_merge (with n_tokens * Hq query heads).
+ *   visible   token t sees the keys of this range below visible + t (any value:
+ *             negative or 0 for a range behind the tokens, >= n for all keys).
+ *   parts     device, f32 [n_tokens][Hq][d + 2], as fathom_sparse_attend_partial
+ *             writes them; the two kinds may be merged with each other.
+ */
+int fathom_store_attend_partial(const fathom_store* K, const fathom_store* V, const void* q, int q_dtype, int n_tokens,
+                                int n_q_heads, int64_t visible, float* parts, void* workspace, size_t workspace_bytes,
+                                fathom_stream_t stream);
+
+/*
+ * fathom_store_attend of several sessions in one pass: session s has stores K[s]
+ * and V[s] (all with the same Hkv and d; lengths and residency may differ, n may
+ * be 0), q device [S][n_tokens][Hq][d], out f32 [S][n_tokens][Hq][d], S <= 64.
+ */
+int fathom_store_attend_batched(const fathom_store* K, const fathom_store* V, int n_sessions, const void* q,
+                                int q_dtype, int n_tokens, int n_q_heads, int causal, float* out, void* workspace,
+                                size_t workspace_bytes, fathom_stream_t stream);
+
+/*
  * Reads and clears this device's status word (FATHOM_DEV_* bits) after
  * synchronising `stream`.  Returns the bits (>= 0), or -FATHOM_ECUDA.
  */

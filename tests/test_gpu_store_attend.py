@@ -1,0 +1,386 @@
+"""Attention over the 4-bit stores (fathom_store_attend, _partial, _batched)
+against the definition in 64 bits.
+
+Tolerance.  The logits are sums over d channels of q Delta code, offsets
+included, so their rounding is relative to A = 15 sum_c |q_c| Delta_c / sqrt(d)
+of the block.  Sixteen channels enter per accumulation step with at most two
+units of the last place of the partial sum (2^-23 A), the split of q Delta into
+two halves of 11 bits adds 2^-22, the scaling of the result 2 roundings: a logit
+is off by at most e = (d/16 + 6) 2^-23 A, and the largest A of any visible
+block serves for all.  The weights then move by a factor of at most e^(2e), and
+exp2 and the sums over keys add at most 2^-22 per step over (n/64 + 64) steps.
+Both act on sum_i p_i 15 Delta_i,c.
+"""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from bit_plane_key_b200 import fathom as F  # noqa: E402
+
+DEV = torch.device("cuda:0")
+
+
+def make_store(n, Hkv, d, seed, spread=1.0, capacity=None, host=False, garbage=False):
+    """A store packed from random rows; with `garbage`, everything behind its last block is filled with other bits."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(Hkv, max(n, 1), d, device=DEV, generator=g)
+    x *= torch.exp(spread * torch.randn(Hkv, 1, d, device=DEV, generator=g))
+    st = F.Store.empty(Hkv, d, capacity or max(n, 1), device=DEV)
+    if garbage:
+        st.planes.random_(generator=g)
+        st.scales.fill_(0x7E00)      # NaN
+    if n:
+        F.append_keys(st, x, n)
+    if host:
+        torch.cuda.synchronize()
+        st = F.Store(st.planes.cpu().pin_memory(), st.scales.cpu().pin_memory(), n, host_resident=True)
+    return st
+
+
+def values(st):
+    """The store's values f64 [Hkv][n][d] and their scales f64 [Hkv][n][d]."""
+    n = st.n
+    bits = np.unpackbits(st.planes.cpu().numpy().view(np.uint8), axis=-1, bitorder="little")[..., :n]
+    code = (bits * np.array([8, 4, 2, 1])[:, None]).sum(2)
+    sc = st.scales.cpu().numpy().view(np.float16).astype(np.float64)
+    sc = np.repeat(sc, 64, axis=-1)[..., :n]
+    return ((code - 7.5) * sc).transpose(0, 2, 1), sc.transpose(0, 2, 1)
+
+
+def reference(ks, vs, q, visible):
+    """f64 out [T][Hq][d], the tolerance of every element, and the maxima and sums (log2 units)."""
+    q = q.double().cpu().numpy()
+    T, Hq, d = q.shape
+    Hkv = ks.n_kv_heads
+    G = Hq // Hkv
+    n = ks.n
+    K, Kd = values(ks)
+    V, Vd = values(vs)
+    out, tol = np.zeros((T, Hq, d)), np.zeros((T, Hq, d))
+    M, L = np.full((T, Hq), -np.inf), np.zeros((T, Hq))
+    for t in range(T):
+        see = max(0, min(n, visible + t))
+        if see == 0:
+            continue
+        for h in range(Hq):
+            g = h // G
+            s = K[g, :see] @ q[t, h] / math.sqrt(d)
+            p = np.exp(s - s.max())
+            M[t, h], L[t, h] = s.max() / math.log(2), p.sum()
+            p /= p.sum()
+            out[t, h] = p @ V[g, :see]
+            A = 15 * (Kd[g, :see] @ np.abs(q[t, h])).max() / math.sqrt(d)
+            e = (d / 16 + 6) * 2.0 ** -23 * A
+            tol[t, h] = (np.expm1(2 * e) + (n / 64 + 64) * 2.0 ** -22) * 15 * (p @ Vd[g, :see])
+    return out, tol, M, L
+
+
+def check(got, ref, tol):
+    got = got.double().cpu().numpy().reshape(ref.shape)
+    assert np.isfinite(got).all()
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), (np.argwhere(bad)[:5], np.abs(got - ref)[bad][:5], tol[bad][:5])
+
+
+def queries(shape, seed, dtype=torch.bfloat16, mult=1.0):
+    g = torch.Generator(device=DEV).manual_seed(1000 + seed)
+    return (torch.randn(*shape, device=DEV, generator=g) * mult).to(dtype)
+
+
+def vis(n, T, causal):
+    return n - T + 1 if causal else n
+
+
+@pytest.mark.parametrize("n", [1, 31, 32, 63, 64, 65, 255, 256, 257, 511, 512, 513, 1000, 4097, 20011])
+def test_lengths(n):
+    ks, vs = make_store(n, 2, 128, n), make_store(n, 2, 128, n + 1)
+    q = queries((8, 128), n)
+    ref, tol, _, _ = reference(ks, vs, q[None], n)
+    check(F.store_attend(ks, vs, q), ref, tol)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_heads_and_dims(d, G, dtype):
+    n = 1500 + d
+    ks, vs = make_store(n, 3, d, d + G), make_store(n, 3, d, d - G)
+    q = queries((3 * G, d), d + G, dtype)
+    ref, tol, _, _ = reference(ks, vs, q[None], n)
+    check(F.store_attend(ks, vs, q), ref, tol)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("T,G,d", [(2, 4, 128), (3, 1, 64), (5, 4, 128), (7, 8, 64), (9, 2, 256), (4, 8, 256), (33, 4, 128),
+                                   (70, 1, 32)])
+def test_tokens(T, G, d, causal):
+    n = 777
+    ks, vs = make_store(n, 2, d, T), make_store(n, 2, d, T + 1)
+    q = queries((T, 2 * G, d), T)
+    ref, tol, _, _ = reference(ks, vs, q, vis(n, T, causal))
+    check(F.store_attend(ks, vs, q, causal=causal), ref, tol)
+
+
+@pytest.mark.parametrize("n,T", [(1, 1), (2, 5), (3, 3), (64, 70), (130, 129), (520, 600)])
+def test_tokens_that_see_no_key_get_zero(n, T):
+    """More tokens than keys: the first tokens see none."""
+    ks, vs = make_store(n, 1, 64, n), make_store(n, 1, 64, T)
+    q = queries((T, 2, 64), T)
+    ref, tol, _, _ = reference(ks, vs, q, n - T + 1)
+    out = F.store_attend(ks, vs, q)
+    check(out, ref, tol)
+    assert (out[:max(0, T - n)] == 0).all()
+
+
+def test_empty_store():
+    ks, vs = make_store(0, 2, 128, 0, garbage=True), make_store(0, 2, 128, 1, garbage=True)
+    assert ks.n == 0
+    out = torch.full((3, 8, 128), 7.0, device=DEV)
+    F.store_attend(ks, vs, queries((3, 8, 128), 0), out=out)
+    assert (out == 0).all()
+    parts = F.store_attend_partial(ks, vs, queries((3, 8, 128), 0), 5)
+    assert (parts[..., 128] == -math.inf).all() and (parts[..., 129] == 0).all()
+
+
+@pytest.mark.parametrize("n", [1, 40, 700, 1025])
+def test_nothing_behind_the_last_block_is_used(n):
+    """Spare capacity, rows behind n: other bits and NaN scales there change nothing."""
+    q = queries((2, 8, 128), n)
+    a = F.store_attend(make_store(n, 2, 128, 5, capacity=5000), make_store(n, 2, 128, 6, capacity=3000), q)
+    b = F.store_attend(make_store(n, 2, 128, 5, capacity=5000, garbage=True),
+                       make_store(n, 2, 128, 6, capacity=3000, garbage=True), q)
+    ks = make_store(n, 2, 128, 5, capacity=5000)
+    # keys of the last block behind n: any code
+    tail = n % 64
+    if tail:
+        w = (n // 64) * 2
+        P = ks.planes.cpu().numpy().view(np.uint32)
+        for i in range(tail, 64):
+            P[..., w + i // 32] |= np.uint32(1 << (i % 32))
+        ks.planes.copy_(torch.from_numpy(P.view(np.int32)).to(DEV))
+    c = F.store_attend(ks, make_store(n, 2, 128, 6, capacity=3000), q)
+    assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("spread,mult", [(3.0, 1.0), (0.5, 30.0), (4.0, 1e-3)])
+def test_wide_channel_scales_and_sharp_weights(spread, mult):
+    n = 3000
+    ks, vs = make_store(n, 2, 128, 9, spread=spread), make_store(n, 2, 128, 10)
+    q = queries((8, 128), 3, torch.float32, mult)
+    ref, tol, _, _ = reference(ks, vs, q[None], n)
+    check(F.store_attend(ks, vs, q), ref, tol)
+
+
+def test_block_scales_from_zero_to_the_largest():
+    """Blocks whose scales are 0, subnormal, ordinary and near the largest f16, in one row of keys."""
+    n, d = 64 * 40, 64
+    ks, vs = make_store(n, 1, d, 20), make_store(n, 1, d, 21)
+    f = torch.tensor([0.0, 6e-8, 1e-6, 1e-3, 1.0, 300.0, 65504.0, 2.0], device=DEV)
+    ks.scales.view(torch.float16)[0, :, :40] = f[torch.arange(40, device=DEV) % 8][None]
+    q = queries((4, d), 1, torch.float32, 1e-4)
+    ref, tol, _, _ = reference(ks, vs, q[None], n)
+    check(F.store_attend(ks, vs, q), ref, tol)
+    vs.scales.view(torch.float16)[0, :, :40] = f[torch.arange(40, device=DEV) * 3 % 8][None]
+    ref, tol, _, _ = reference(ks, vs, q[None], n)
+    check(F.store_attend(ks, vs, q), ref, tol)
+
+
+@pytest.mark.parametrize("mult", [0.0, 1e-30, 1e30])
+def test_query_magnitudes(mult):
+    """Zero queries weigh every key alike; huge ones choose one key (equal logits share)."""
+    n = 900
+    ks, vs = make_store(n, 2, 128, 30), make_store(n, 2, 128, 31)
+    q = queries((4, 128), 2, torch.float32) * mult
+    out = F.store_attend(ks, vs, q).double().cpu().numpy()
+    if mult == 1e30:
+        K, _ = values(ks)
+        V, _ = values(vs)
+        qn = q.double().cpu().numpy()
+        for h in range(4):
+            s = np.sort(K[h // 2] @ qn[h])
+            assert s[-1] - s[-2] > 1e-4 * abs(s[-1])       # one winner, beyond rounding
+            i = int(np.argmax(K[h // 2] @ qn[h]))
+            assert np.abs(out[h] - V[h // 2, i]).max() <= 64 * 2.0 ** -22 * 15 * np.abs(V[h // 2, i]).max()
+    else:
+        ref, tol, _, _ = reference(ks, vs, q[None], n)
+        check(torch.from_numpy(out), ref, tol)
+
+
+def test_partials_of_ranges_merge_to_the_whole():
+    n, T, G = 3000, 3, 4
+    ks, vs = make_store(n, 2, 128, 40), make_store(n, 2, 128, 41)
+    q = queries((T, 2 * G, 128), 4)
+    ref, tol, M, L = reference(ks, vs, q, n - T + 1)
+    cuts = [0, 1024, 2048, 2048, n]
+    parts = []
+    for a, b in zip(cuts, cuts[1:]):
+        m = max(1, -(-(b - a) // 1024)) * 1024
+        def sub(st):
+            P = torch.zeros(2, 128, 4, m // 32, dtype=torch.int32, device=DEV)
+            S = torch.zeros(2, 128, m // 64, dtype=torch.int16, device=DEV)
+            P[..., :(b - a + 31) // 32] = st.planes[..., a // 32:(b + 31) // 32]
+            S[..., :(b - a + 63) // 64] = st.scales[..., a // 64:(b + 63) // 64]
+            return F.Store(P, S, b - a)
+        parts.append(F.store_attend_partial(sub(ks), sub(vs), q, n - T + 1 - a))
+    merged = F.attend_merge(torch.stack(parts).view(len(parts), T * 2 * G, 130))
+    check(merged, ref, tol)
+    whole = F.store_attend_partial(ks, vs, q, n - T + 1).double().cpu().numpy()
+    m, l = whole[..., 128], whole[..., 129]
+    # o is relative to 2^m, l alike
+    o = whole[..., :128] / l[..., None]
+    assert (np.abs(o - ref) <= tol).all()
+    assert np.allclose(m + np.log2(l), M + np.log2(L), rtol=0, atol=1e-3)
+
+
+def test_partial_of_a_store_merges_with_a_partial_of_rows():
+    """Old keys in 4 bits, the newest in bf16: the two kinds of partials share their units."""
+    n, Hkv, G, d = 1024, 2, 2, 128
+    ks, vs = make_store(n, Hkv, d, 50), make_store(n, Hkv, d, 51)
+    q = queries((Hkv * G, d), 5)
+    Kr, Vr = F.kv_rows(Hkv, 50, d, device=DEV)
+    Kr.copy_(torch.randn(Hkv, 50, d, device=DEV))
+    Vr.copy_(torch.randn(Hkv, 50, d, device=DEV))
+    idx = torch.arange(50, dtype=torch.int32, device=DEV).repeat(Hkv * G, 1)
+    p = torch.stack([F.store_attend_partial(ks, vs, q, n), F.sparse_attend_partial(q, Kr, Vr, idx, 0)])
+    out = F.attend_merge(p).double().cpu().numpy()
+    K = np.concatenate([values(ks)[0], Kr.double().cpu().numpy()], 1)
+    V = np.concatenate([values(vs)[0], Vr.double().cpu().numpy()], 1)
+    qn = q.double().cpu().numpy()
+    for h in range(Hkv * G):
+        s = K[h // G] @ qn[h] / math.sqrt(d)
+        w = np.exp(s - s.max())
+        o = (w / w.sum()) @ V[h // G]
+        assert np.linalg.norm(out[h] - o) <= 1e-3 * np.linalg.norm(o)
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_batched_sessions(T):
+    lens = [1, 5000, 0, 64, 513, 2, 12000, 1024, 77]
+    ks = [make_store(n, 2, 128, 60 + i, capacity=n + 100 * i) for i, n in enumerate(lens)]
+    vs = [make_store(n, 2, 128, 160 + i) for i, n in enumerate(lens)]
+    ks[3] = ks[3].to_host()
+    vs[6] = vs[6].to_host()
+    q = queries((len(lens), T, 8, 128), 6)
+    out = F.store_attend_batched(ks, vs, q)
+    full = F.store_attend_batched(ks, vs, q, causal=False)
+    for s, n in enumerate(lens):
+        for o, causal in ((out, True), (full, False)):
+            ref, tol, _, _ = reference(ks[s], vs[s], q[s], vis(n, T, causal))
+            check(o[s], ref, tol)
+
+
+def test_sixty_four_sessions():
+    ks = [make_store(1 + 37 * i, 1, 64, i) for i in range(64)]
+    vs = [make_store(1 + 37 * i, 1, 64, 100 + i) for i in range(64)]
+    q = queries((64, 1, 8, 64), 7)
+    out = F.store_attend_batched(ks, vs, q)
+    for s in range(64):
+        ref, tol, _, _ = reference(ks[s], vs[s], q[s], ks[s].n)
+        check(out[s], ref, tol)
+
+
+def test_host_resident_stores_give_the_same_bits():
+    ks, vs = make_store(2500, 2, 128, 70), make_store(2500, 2, 128, 71)
+    q = queries((2, 8, 128), 8)
+    a = F.store_attend(ks, vs, q)
+    assert torch.equal(a, F.store_attend(ks.to_host(), vs.to_host(), q))
+    assert torch.equal(a, F.store_attend(ks, vs.to_host(), q))
+
+
+def test_same_bits_on_every_call_and_from_a_dirty_workspace():
+    ks, vs = make_store(50000, 4, 128, 80), make_store(50000, 4, 128, 81)
+    q = queries((16, 128), 9)
+    ws = torch.empty(F.store_attend_workspace_bytes(ks, 1, 1, 16), dtype=torch.uint8, device=DEV)
+    first = F.store_attend(ks, vs, q, workspace=ws)
+    for b in (0, 255, 127):
+        ws.fill_(b)
+        assert torch.equal(first, F.store_attend(ks, vs, q, workspace=ws))
+    sub = F.store_attend(ks, vs, q[:4].repeat(4, 1).contiguous())
+    assert sub.shape == first.shape
+
+
+def test_streams_and_graphs():
+    """Two streams with a workspace each, and two captured graphs replayed in turn after the stores have grown."""
+    n = 3000
+    ks, vs = make_store(n, 2, 128, 90), make_store(n, 2, 128, 91)
+    qa, qb = queries((8, 128), 10), queries((8, 128), 11)
+    a, b = F.store_attend(ks, vs, qa), F.store_attend(ks, vs, qb)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            a1 = F.store_attend(ks, vs, qa)
+        with torch.cuda.stream(s2):
+            b1 = F.store_attend(ks, vs, qb)
+        torch.cuda.synchronize()
+        assert torch.equal(a, a1) and torch.equal(b, b1)
+    ws = torch.empty(F.store_attend_workspace_bytes(ks, 1, 1, 8), dtype=torch.uint8, device=DEV)
+    oa, ob = torch.empty_like(a), torch.empty_like(b)
+    graphs = []
+    for q, o in ((qa, oa), (qb, ob)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            F.store_attend(ks, vs, q, out=o, workspace=ws)     # the two share a workspace: replayed one after the other
+        graphs.append(g)
+    for _ in range(3):
+        oa.zero_(), ob.zero_()
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, oa) and torch.equal(b, ob)
+    other = make_store(n, 2, 128, 95)
+    ks.planes.copy_(other.planes)
+    ks.scales.copy_(other.scales)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(oa, F.store_attend(ks, vs, qa))
+
+
+def test_long_row_over_many_ctas():
+    """One KV head over 300000 keys: its tiles spread over the whole GPU."""
+    n = 300001
+    ks, vs = make_store(n, 1, 64, 99), make_store(n, 1, 64, 98)
+    q = queries((1, 4, 64), 12)
+    ref, tol, _, _ = reference(ks, vs, q, n)
+    check(F.store_attend(ks, vs, q), ref, tol)
+
+
+def test_refusals():
+    ks, vs = make_store(100, 2, 64, 1), make_store(100, 2, 64, 2)
+    q = queries((8, 64), 0)
+    with pytest.raises(F.FathomError):
+        F.store_attend(ks, make_store(101, 2, 64, 3), q)           # lengths differ
+    with pytest.raises(F.FathomError):
+        F.store_attend(ks, make_store(100, 1, 64, 3), q)           # heads differ
+    with pytest.raises(F.FathomError):
+        F.store_attend(ks, vs, queries((6, 64), 0))                # three heads to a KV head
+    with pytest.raises(F.FathomError) as e:
+        F.store_attend(make_store(10, 1, 96, 1), make_store(10, 1, 96, 2), queries((1, 96), 0))
+    assert e.value.status == F.EUNSUPPORTED
+    with pytest.raises(F.FathomError) as e:
+        F.store_attend(ks, vs, q, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+    assert e.value.status == F.ENOMEM
+    ws = torch.empty(F.store_attend_workspace_bytes(ks, 1, 1, 8) + 256, dtype=torch.uint8, device=DEV)
+    with pytest.raises(F.FathomError):
+        F.store_attend(ks, vs, q, workspace=ws[1:])                # misaligned
+    with pytest.raises(F.FathomError):
+        F.store_attend(ks, vs, q.cpu())
+    with pytest.raises(F.FathomError):
+        F.store_attend(F.Store(ks.planes.cpu(), ks.scales.cpu(), 100, host_resident=True), vs, q)   # not page-locked
+    with pytest.raises(TypeError):
+        F.store_attend(ks, vs, q.half())
+    with pytest.raises(ValueError):
+        F.store_attend(ks, vs, queries((64, 8), 0).t())
+    with pytest.raises(ValueError):
+        F.store_attend(ks, vs, q, out=torch.empty(8, 64, device=DEV, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        F.store_attend_batched([ks], [vs, vs], q[None, None])
+    with pytest.raises(F.FathomError):
+        F.store_attend_batched([ks] * 65, [vs] * 65, q[None, None].repeat(65, 1, 1, 1))
