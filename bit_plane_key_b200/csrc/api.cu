@@ -573,26 +573,38 @@ int store_attend(const fathom_store* Ks, const fathom_store* Vs, int S, const vo
     if (d != 32 && d != 64 && d != 128 && d != 256) return FATHOM_EUNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(ws) & 255) return FATHOM_EINVAL;
     if (ws_bytes < store_attend_workspace_bytes(S, T, Hq, Hkv, d)) return FATHOM_ENOMEM;
-    AttendMap m;
-    m.nsess = S;
+    // sessions go in groups of kAttendSets, one launch each
+    constexpr int kGroups = (kMaxSets + kAttendSets - 1) / kAttendSets;
+    AttendMap maps[kGroups];
     for (int s = 0; s < S; ++s) {
+        AttendMap& m = maps[s / kAttendSets];
+        const int e = s % kAttendSets;
         const fathom_store &k = Ks[s], &v = Vs[s];
         if (k.n_kv_heads != Hkv || v.n_kv_heads != Hkv || k.d != d || v.d != d || k.n != v.n || k.n > INT32_MAX)
             return FATHOM_EINVAL;
         // an empty store needs no arrays' contents, but is checked like any other
-        int rc = resolve_growing(&k, k.n > 0 ? k.n : 1, &m.k_planes[s], &m.k_scales[s]);
-        if (!rc) rc = resolve_growing(&v, v.n > 0 ? v.n : 1, &m.v_planes[s], &m.v_scales[s]);
+        int rc = resolve_growing(&k, k.n > 0 ? k.n : 1, &m.k_planes[e], &m.k_scales[e]);
+        if (!rc) rc = resolve_growing(&v, v.n > 0 ? v.n : 1, &m.v_planes[e], &m.v_scales[e]);
         if (rc) return rc;
-        m.k_pad[s] = k.n_pad;
-        m.v_pad[s] = v.n_pad;
-        m.n[s] = k.n;
+        m.k_pad[e] = k.n_pad;
+        m.v_pad[e] = v.n_pad;
+        m.n[e] = k.n;
         int64_t vis = visible ? visible[s] : (causal ? k.n - T + 1 : k.n);
         if (vis > k.n) vis = k.n;
         if (vis < -T) vis = -T;   // no token sees a key
-        m.visible[s] = vis;
+        m.visible[e] = vis;
+        m.nsess = e + 1;
     }
     if (!is_here(q) || !is_here(dst) || !is_here(ws)) return FATHOM_EINVAL;
-    return to_status(launch_store_attend(m, Hkv, d, q, q_dtype, T, Hq, out, parts, ws, (cudaStream_t)stream));
+    if (!device_status_ptr()) return FATHOM_ECUDA;
+    const size_t rows = (size_t)kAttendSets * T * Hq;   // of a group
+    for (int i = 0; i * kAttendSets < S; ++i) {
+        const void* qi = static_cast<const char*>(q) + i * rows * d * (q_dtype == FATHOM_F32 ? 4 : 2);
+        const cudaError_t e = launch_store_attend(maps[i], Hkv, d, qi, q_dtype, T, Hq, out ? out + i * rows * d : nullptr,
+                                                  parts ? parts + i * rows * (d + 2) : nullptr, ws, (cudaStream_t)stream);
+        if (e != cudaSuccess) return FATHOM_ECUDA;
+    }
+    return FATHOM_OK;
 }
 }  // namespace
 

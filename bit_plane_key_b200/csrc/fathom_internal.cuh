@@ -1,6 +1,7 @@
 // Internal declarations shared by the CUDA translation units of libfathom.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -205,18 +206,22 @@ cudaError_t launch_append_rows(const uint16_t* K_rows, uint32_t* k_planes, uint1
 // Sessions of an attention over stores: query token t of session s sees the
 // keys below min(n[s], visible[s] + t).  launch_store_attend fills tiles (per
 // row of session s) and unit0 (prefix sums over the sessions' rows).
+constexpr int kAttendSets = 32;   // sessions of a launch
 struct AttendMap {
+    // planes and scales of K and V, made by launch_store_attend
+    alignas(64) CUtensorMap k_tm[kAttendSets], ks_tm[kAttendSets], v_tm[kAttendSets], vs_tm[kAttendSets];
     int nsess;
-    const uint32_t* k_planes[kMaxSets];
-    const uint16_t* k_scales[kMaxSets];
-    const uint32_t* v_planes[kMaxSets];
-    const uint16_t* v_scales[kMaxSets];
-    int64_t k_pad[kMaxSets];
-    int64_t v_pad[kMaxSets];
-    int64_t n[kMaxSets];
-    int64_t visible[kMaxSets];
-    int tiles[kMaxSets];
-    int64_t unit0[kMaxSets + 1];
+    const uint32_t* k_planes[kAttendSets];
+    const uint16_t* k_scales[kAttendSets];
+    const uint32_t* v_planes[kAttendSets];
+    const uint16_t* v_scales[kAttendSets];
+    int64_t k_pad[kAttendSets];
+    int64_t v_pad[kAttendSets];
+    int64_t n[kAttendSets];
+    int64_t visible[kAttendSets];
+    int tiles[kAttendSets];
+    int unit0[kAttendSets + 1];
+    int each, more;   // units of a CTA, and CTAs with one more
 };
 size_t store_attend_workspace_bytes(int S, int T, int Hq, int Hkv, int d);
 // parts non-null: per-row partials [S][T][Hq][d + 2] instead of out

@@ -34,30 +34,49 @@
 namespace fathom {
 namespace {
 
-constexpr int kTileBlocks = 8;                  // one per warp
-constexpr int kTile = kTileBlocks * kBlock;
-constexpr int kThreads = 32 * kTileBlocks;
 constexpr int kTilePairs = 4;                   // queries per 8 columns
-constexpr int kMaxCtas = 592;                   // bound for the workspace: 148 SMs, four CTAs each
+constexpr int kMaxCtas = 296;                   // two CTAs per SM
+constexpr int kWarps = 8;                       // of a CTA
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = kWarps * 2 * kBlock;      // keys: two blocks per warp, 128 bytes of every plane row
 
-template <int D, int NT>
+template <int D, int NT, bool F32>
 struct Shape {
+    static constexpr int kCtas = (NT == 1 && D <= 128) ? 2 : 1;   // per SM
     static constexpr int kPairs = kTilePairs * NT;          // (token, head of the group) pairs of a set
-    static constexpr int kBlkWords = D * 8 + 4;             // code words of a block, 4 of padding against bank conflicts
-    static constexpr int kCodes = kTileBlocks * kBlkWords;  // of K, and of V
-    static constexpr int kScaleHalves = kTileBlocks * D;
-    static constexpr size_t kSmem = 4 * (size_t)(2 * kCodes) + 2 * 2 * kScaleHalves + 4 * (size_t)(kPairs * D) +
-                                    4 * (size_t)(2 * kTileBlocks * kPairs + kPairs);
-    static constexpr int kCtasPerSm = (D == 256 || NT == 4) ? 1 : 2;
-    // the warps' partial outputs reuse the code words
-    static_assert(kTileBlocks * kPairs * D <= 2 * kCodes, "partial outputs fit");
+    static constexpr int KS = D / 16;                       // 16-channel steps
+    // a chunk: the tile's planes of CH channels of one operand; channels l and
+    // l + HP of it are a pair
+    static constexpr int CH = 32, CK = CH / 16, NC = D / CH, HP = CH / 2;
+    static constexpr int kRaw = CH * 4 * (kTile / 32);      // words of a chunk's planes
+    static constexpr int kRawScales = D * (kTile / kBlock); // halves of a tile's scales, of K or V
+    static constexpr int kRing = 4;
+    static constexpr int kCodes = 2 * CH * 8;               // words of a warp's codes of a chunk
+    static constexpr int kOwn = kCodes > kPairs * D ? kCodes : kPairs * D;   // or of its partial outputs
+    static constexpr int kScales = 2 * 2 * D;               // halves: K, V; block; channels, pair by pair
+    static constexpr int kQWords = NT * KS * 32 * 4;        // a lane's share of the queries
+    static constexpr int kQ2Words = F32 ? kQWords / 2 : 0;
+    static constexpr size_t kBytes = 4 * (size_t)(kRing * kRaw + kWarps * kOwn) + 2 * (size_t)(kWarps * kScales + 2 * kRawScales) +
+                                     4 * (size_t)(kQWords + kQ2Words) + 4 * (size_t)(2 * kWarps * kPairs + kPairs) +
+                                     8 * 2 * (kRing + 1);
+    static constexpr size_t kSmem = kBytes + 1024;          // the planes start on a 1024-byte boundary
 };
 
-// first unit of run p of P over U units, and the run of a unit
-__device__ __forceinline__ int64_t run_start(int64_t p, int64_t U, int64_t P) { return p * U / P; }
-__device__ __forceinline__ int64_t run_of(int64_t u, int64_t U, int64_t P) { return ((u + 1) * P - 1) / U; }
+// where channel c of D lies when channels are listed pair by pair
+template <int CH>
+__device__ __forceinline__ int paired(int c) {
+    const int l = c % CH;
+    return c - l + 2 * (l % (CH / 2)) + l / (CH / 2);
+}
 
-__device__ __forceinline__ int session_of_unit(const AttendMap& m, int64_t u) {
+// units are cut into runs: the first `more` of U / P + 1, the others of U / P = each
+__device__ __forceinline__ int run_start(const AttendMap& m, int p) { return p * m.each + (p < m.more ? p : m.more); }
+__device__ __forceinline__ int run_of(const AttendMap& m, int u) {
+    const int big = m.more * (m.each + 1);
+    return u < big ? u / (m.each + 1) : m.more + (u - big) / m.each;
+}
+
+__device__ __forceinline__ int session_of_unit(const AttendMap& m, int u) {
     int lo = 0, hi = m.nsess;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -68,10 +87,15 @@ __device__ __forceinline__ int session_of_unit(const AttendMap& m, int64_t u) {
 }
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, const uint32_t* b) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// with the operand B's bits in floats
+__device__ __forceinline__ void mma_p(float* c, const uint32_t* a, const float* b) {
+    const uint32_t bits[2] = {__float_as_uint(b[0]), __float_as_uint(b[1])};
+    mma(c, a, bits);
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
@@ -83,6 +107,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// loads that stay where they are written: ahead of the work that hides them
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 // (low, high) as two fp16
 __device__ __forceinline__ uint32_t half2_of(float low, float high) {
     uint32_t r;
@@ -92,14 +118,66 @@ __device__ __forceinline__ uint32_t half2_of(float low, float high) {
 // the leading 11 significant bits
 __device__ __forceinline__ float leading11(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFFE000u); }
 
+// x where mask has a bit, else y; one instruction, where the expression takes two
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y, uint32_t mask) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(x), "r"(y), "r"(mask));
+    return r;
+}
+
+// The ring of raw planes: a chunk's bytes arrive by one asynchronous tensor
+// copy.  A wait gives up after 2^22 tries (seconds), which no correct run reaches.
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void barrier_init(uint64_t* b, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool barrier_try(uint64_t* b, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(smem_addr(b)), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool barrier_wait(uint64_t* b, uint32_t parity) {
+    if (barrier_try(b, parity)) return true;
+    for (int i = 0; i < (1 << 22); ++i)
+        if (barrier_try(b, parity)) return true;
+    return false;
+}
+// bytes to come before the barrier's phase is over
+__device__ __forceinline__ void barrier_expect(uint64_t* b, uint32_t bytes) {
+    asm volatile("{ .reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1; }" ::"r"(smem_addr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_planes(void* dst, const CUtensorMap* tm, int word, int channel, uint64_t* b) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(tm), "r"(word), "r"(channel), "r"(0), "r"(smem_addr(b))
+        : "memory");
+}
+__device__ __forceinline__ void copy_scales(void* dst, const CUtensorMap* tm, int block, int channel, uint64_t* b) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_addr(dst)),
+        "l"(tm), "r"(block), "r"(channel), "r"(smem_addr(b))
+        : "memory");
+}
+// this warp has read what the barrier's buffer held
+__device__ __forceinline__ void barrier_arrive(uint64_t* b) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        asm volatile("{ .reg .b64 t; mbarrier.arrive.shared::cta.b64 t, [%0]; }" ::"r"(smem_addr(b)) : "memory");
+}
+
 // plane words W[j] of 32 keys -> N[r]: nibble m = code of key 4 m + r
 __device__ __forceinline__ void planes_to_nibbles(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t* N) {
-    const uint32_t E = ((w0 << 1) & 0xAAAAAAAAu) | (w1 & 0x55555555u), O = (w0 & 0xAAAAAAAAu) | ((w1 >> 1) & 0x55555555u);
-    const uint32_t F = ((w2 << 1) & 0xAAAAAAAAu) | (w3 & 0x55555555u), H = (w2 & 0xAAAAAAAAu) | ((w3 >> 1) & 0x55555555u);
-    N[0] = ((E << 2) & 0xCCCCCCCCu) | (F & 0x33333333u);
-    N[2] = (E & 0xCCCCCCCCu) | ((F >> 2) & 0x33333333u);
-    N[1] = ((O << 2) & 0xCCCCCCCCu) | (H & 0x33333333u);
-    N[3] = (O & 0xCCCCCCCCu) | ((H >> 2) & 0x33333333u);
+    const uint32_t E = pick(w0 << 1, w1, 0xAAAAAAAAu), O = pick(w0, w1 >> 1, 0xAAAAAAAAu);
+    const uint32_t F = pick(w2 << 1, w3, 0xAAAAAAAAu), H = pick(w2, w3 >> 1, 0xAAAAAAAAu);
+    N[0] = pick(E << 2, F, 0xCCCCCCCCu);
+    N[2] = pick(E, F >> 2, 0xCCCCCCCCu);
+    N[1] = pick(O << 2, H, 0xCCCCCCCCu);
+    N[3] = pick(O, H >> 2, 0xCCCCCCCCu);
 }
 
 // operand value pairs p = 0..3 of a word of codes (odd p: 16 times the code)
@@ -112,358 +190,477 @@ __device__ __forceinline__ void operand(const uint4& raw, int p, uint32_t* a) {
     a[3] = (raw.w >> sh) & mask;
 }
 
-// Where the keys of a tile lie in the operands (block b = its warp): key
-// 32 w + 4 (p + 4 k4) + r of the block is nibble p of half k4 of N[r] of word w.
+// Where the keys of a block lie in the operands: key 32 w + 4 (p + 4 k4) + r is
+// nibble p of half k4 of N[r] of word w.
 //   S: row g = 2 r + k4 (w = 0) or that plus 8 (w = 1) of m-tile p; a lane's
-//      columns k are the channels 16 ks + 4 t + 0..3.
-//   O: row g is channel 16 mt + 2 g, row g + 8 the next; k-step p, column
-//      pair t is r = t, k4 = 0 and 1, w = 0 then w = 1.
+//      columns k are the channel pairs 8 ks + 2 t and the one behind it.
+//   O: row g is the first channel of pair 8 mt + g, row g + 8 the second; k-step
+//      p, column pair t is r = t, k4 = 0 and 1, w = 0 then w = 1.
 // Both orders meet: the transposed S accumulators of rows g = 2 t, 2 t + 1 are
 // the P operand's k columns 2 t, 2 t + 1.
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
-store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restrict__ q, int q_dtype, int T, int Hq,
-                    int Hkv, int sets, float* __restrict__ slots, float* __restrict__ out, float* __restrict__ parts) {
-    using Sh = Shape<D, NT>;
-    constexpr int KS = D / 16;        // 16-channel steps
-    constexpr int kPairs = Sh::kPairs;
-    extern __shared__ __align__(16) uint32_t smem[];
-    uint32_t* s_k = smem;                               // [block][ks][lane][4] code words
-    uint32_t* s_v = s_k + Sh::kCodes;                   // [block][mt][lane][4]
-    uint16_t* s_ks = reinterpret_cast<uint16_t*>(s_v + Sh::kCodes);   // [block][D] scales
-    uint16_t* s_vs = s_ks + Sh::kScaleHalves;
-    float* s_q = reinterpret_cast<float*>(s_vs + Sh::kScaleHalves);   // [NT][ks][4 pairs][16 channels]
-    float* s_m = s_q + kPairs * D;                      // [warp][pair]
-    float* s_l = s_m + kTileBlocks * kPairs;
-    float* s_f = s_l + kTileBlocks * kPairs;            // [pair] 1 / the query's normalisation
+// A row of tiles: one KV head of one session, for one set of queries.
+struct Row {
+    int s, g, set, row;
+    int u0, u1;   // its units
+};
+__device__ __noinline__ Row row_of(const AttendMap& map, int u, int Hkv, int sets) {
+    Row r;
+    r.s = session_of_unit(map, u);
+    const int tiles = map.tiles[r.s];
+    const int rl = (u - map.unit0[r.s]) / tiles;
+    r.g = rl / sets;
+    r.set = rl - r.g * sets;
+    r.row = r.s * Hkv * sets + rl;
+    r.u0 = map.unit0[r.s] + rl * tiles;
+    r.u1 = r.u0 + tiles;
+    return r;
+}
 
-    const int64_t U = map.unit0[map.nsess], P = gridDim.x;
-    const int64_t u1 = run_start(blockIdx.x + 1, U, P);
-    int64_t u = run_start(blockIdx.x, U, P);
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, Shape<D, NT, F32>::kCtas)
+store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restrict__ q, int q_dtype, int T, int Hq,
+                    int Hkv, int sets, float* __restrict__ slots, float* __restrict__ out, float* __restrict__ parts,
+                    unsigned int* status) {
+    using Sh = Shape<D, NT, F32>;
+    constexpr int KS = Sh::KS, CH = Sh::CH, CK = Sh::CK, NC = Sh::NC, HP = Sh::HP, kPairs = Sh::kPairs, kRing = Sh::kRing;
+    extern __shared__ uint32_t smem_raw[];
+    uint32_t* s_raw = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u) / 4;   // the next 1024-byte boundary
+    // [ring][plane][channel][32 words], 16-byte pieces of a row swizzled by the channel's low 3 bits
+    uint32_t* s_codes = s_raw + kRing * Sh::kRaw;       // [warp][block][ks][lane][4] code words
+    uint16_t* s_rs = reinterpret_cast<uint16_t*>(s_codes + kWarps * Sh::kOwn);     // [K, V][D][blocks of the tile] scales, 16-byte pieces swizzled by the channel's bit 2
+    uint16_t* s_sc = s_rs + 2 * Sh::kRawScales;         // [warp][K, V][block][D] scales
+    uint32_t* s_q = reinterpret_cast<uint32_t*>(s_sc + kWarps * Sh::kScales);      // [NT][ks][lane][4]
+    uint32_t* s_q2 = s_q + Sh::kQWords;                 // [NT][ks][lane][2], f32 queries only
+    float* s_m = reinterpret_cast<float*>(s_q2 + Sh::kQ2Words);   // [warp][pair]
+    float* s_l = s_m + kWarps * kPairs;
+    float* s_f = s_l + kWarps * kPairs;                 // [pair] the query's part of the logits' factor
+    uint64_t* s_full = reinterpret_cast<uint64_t*>(s_f + kPairs);   // [ring] the chunk has arrived; then the scales
+    uint64_t* s_read = s_full + kRing + 1;              // every warp has read it
+
+    const int ub = run_start(map, blockIdx.x);
+    const int units = run_start(map, blockIdx.x + 1) - ub, chunks = units * (2 * NC);
     const int G = Hq / Hkv, C = T * G;
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int lg = lane >> 2, lt = lane & 3;            // g and t of the operand layouts
-    const bool low = lg & 1;                            // this lane's column is the low half of its query
 
-    while (u < u1) {
-        const int s = session_of_unit(map, u);
-        const int tiles = map.tiles[s];
-        const int rl = (int)((u - map.unit0[s]) / tiles);
-        const int g = rl / sets, set = rl % sets;
-        const int64_t row = (int64_t)s * Hkv * sets + rl;
-        const int64_t row0 = map.unit0[s] + (int64_t)rl * tiles, row1 = row0 + tiles;
-        const int64_t ue = row1 < u1 ? row1 : u1;
-        const bool whole = u == row0 && ue == row1;     // no other CTA has a share of this row
-        const int64_t kw = map.k_pad[s] / 32, vw = map.v_pad[s] / 32;
-        const uint32_t* Kp = map.k_planes[s] + (int64_t)g * D * 4 * kw;
-        const uint16_t* Ks = map.k_scales[s] + (int64_t)g * D * (kw / 2);
-        const uint32_t* Vp = map.v_planes[s] + (int64_t)g * D * 4 * vw;
-        const uint16_t* Vs = map.v_scales[s] + (int64_t)g * D * (vw / 2);
+    // copies chunk c of a unit (NC chunks of K, then NC of V) of row r to ring buffer i
+    auto copy = [&](const Row& r, int unit, int c, int i) {
+        barrier_expect(s_full + i, 4 * Sh::kRaw);
+        copy_planes(s_raw + i * Sh::kRaw, c < NC ? &map.k_tm[r.s] : &map.v_tm[r.s], (unit - r.u0) * (kTile / 32),
+                    r.g * D + (c < NC ? c : c - NC) * CH, s_full + i);
+    };
+    auto copy_scale = [&](const Row& r, int unit) {
+        const int b = (unit - r.u0) * (kTile / kBlock);
+        barrier_expect(s_full + kRing, 2 * 2 * Sh::kRawScales);
+        copy_scales(s_rs, &map.ks_tm[r.s], b, r.g * D, s_full + kRing);
+        copy_scales(s_rs + Sh::kRawScales, &map.vs_tm[r.s], b, r.g * D, s_full + kRing);
+    };
+    Row rw = row_of(map, ub, Hkv, sets);
+    if (threadIdx.x == kThreads - 32) {                 // the first queries go to other warps
+        for (int i = 0; i <= kRing; ++i) {
+            barrier_init(s_full + i, 1);
+            barrier_init(s_read + i, kWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        copy_scale(rw, ub);
+        for (int i = 0; i < kRing && i < chunks; ++i) {
+            const int unit = ub + i / (2 * NC);
+            copy(unit < rw.u1 ? rw : row_of(map, unit, Hkv, sets), unit, i % (2 * NC), i);
+        }
+    }
+
+    bool stuck = false;
+    uint32_t* codes = s_codes + wp * Sh::kOwn;
+    uint16_t* scales = s_sc + wp * Sh::kScales;
+    int u = 0, j = 0;
+    while (u < units) {
+        const int s = rw.s;
+        const int left = rw.u1 - ub, re = left < units ? left : units;
+        const bool whole = ub + u == rw.u0 && left <= units;   // no other CTA has a share of this row
         const int n = (int)map.n[s];
 
-        // the set's queries, each divided by a power of two to at most 1 to 2 in magnitude
-        __syncthreads();
-        for (int x = wp; x < kPairs; x += kTileBlocks) {
-            const int pr = set * kPairs + x;
-            float v[(D + 31) / 32];
+        // the set's queries in fp16, each scaled by a power of two to at most 2^6 to 2^7
+        // in magnitude (so that the least fp16 is 2^-31 of it): q1 = the value's first
+        // 11 bits, for f32 queries q2 = the next 11
+        for (int x = wp; x < kPairs; x += kWarps) {
+            const int pr = rw.set * kPairs + x;
+            float v[D / 32];
             float mx = 0.0f;
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
-                v[e] = pr < C ? load_q(q, q_dtype, (((int64_t)s * T + pr / G) * Hq + g * G + pr % G) * D + 32 * e + lane) : 0.0f;
+                v[e] = pr < C ? load_q(q, q_dtype, (((int64_t)s * T + pr / G) * Hq + rw.g * G + pr % G) * D + 32 * e + lane) : 0.0f;
                 mx = fmaxf(mx, fabsf(v[e]));
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            int ex = 0;
-            if (mx > 0.0f) ex = ilogbf(mx);
+            // 2^-120 and below count as 0
+            const int ex = max((int)(__float_as_uint(mx) >> 23) - 133, -126);
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
-                const int c = 32 * e + lane;
-                s_q[(((x >> 2) * KS + (c >> 4)) * 4 + (x & 3)) * 16 + (c & 15)] = ldexpf(v[e], -ex);
+                const int c = paired<CH>(32 * e + lane);
+                const float vn = v[e] * down;
+                const __half q1 = __float2half_rn(vn);
+                // columns 2x and 2x + 1 of the 8; for the latter the operand is q1 d - rn(q1 d)
+                const int base = ((x >> 2) * KS + (c >> 4)) * 32 + (x & 3) * 8 + ((c >> 2) & 3);   // lane of column 2x
+                __half* h0 = reinterpret_cast<__half*>(s_q + base * 4) + (c & 3);
+                __half* h1 = h0 + 4 * 8;
+                h0[0] = q1;
+                h0[4] = __float2half_rn(0.0f);
+                h1[0] = __hneg(q1);
+                h1[4] = q1;
+                if (F32) {
+                    __half* g0 = reinterpret_cast<__half*>(s_q2 + base * 2) + (c & 3);
+                    g0[0] = __float2half_rn(0.0f);
+                    g0[4 * 4] = __float2half_rn(vn - __half2float(q1));
+                }
             }
             // logits in log2 units = sums of products * this * 2^24 / the block's factor;
             // never 0, which a masked score of -inf would turn into NaN
-            if (lane == 0) s_f[x] = fmaxf(ldexpf(1.4426950408889634f / sqrtf((float)D), ex), 1.17549435e-38f);
+            if (lane == 0) s_f[x] = fmaxf(1.4426950408889634f / sqrtf((float)D) * __uint_as_float((uint32_t)(127 + ex) << 23), 1.17549435e-38f);
         }
 
         float O[NT][KS][2], m[NT], l[NT];
-        int limit[NT], least = n;
+        int limit[NT], least = n, most;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt] = -INFINITY;
             l[nt] = 0.0f;
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt) O[nt][mt][0] = O[nt][mt][1] = 0.0f;
-            const int64_t see = map.visible[s] + (set * kPairs + nt * kTilePairs + lt) / G;
+            const int64_t see = map.visible[s] + (rw.set * kPairs + nt * kTilePairs + lt) / G;
             limit[nt] = (int)(see < n ? (see > 0 ? see : 0) : n);
         }
-        {   // the set's first pair sees the fewest keys
-            const int64_t see = map.visible[s] + set * kPairs / G;
+        {   // the set's first pair sees the fewest keys, its last the most
+            int64_t see = map.visible[s] + rw.set * kPairs / G;
             if (see < n) least = (int)(see > 0 ? see : 0);
+            see = map.visible[s] + (rw.set * kPairs + kPairs - 1) / G;
+            most = (int)(see < n ? (see > 0 ? see : 0) : n);
         }
+        __syncthreads();                                // the queries are in place
 
-        for (; u < ue; ++u) {
-            const int i0 = (int)(u - row0) * kTile;
-            __syncthreads();                            // the tile before has been read
-            // ---- codes and scales of the tile into shared memory
+        for (; u < re; ++u) {
+            const int k0 = (ub + u - rw.u0) * kTile + 2 * wp * kBlock;   // the warp's first block
+            const bool act = k0 < most;
+            // ---- the blocks' scales: 0 behind the last block that is seen, where memory may hold anything
+            __half2 sc2[2];
+            float back[2];
+            __syncwarp();
             {
-                const int b = lane & 7;                 // a lane's block; its channels: four in a row
-#pragma unroll
-                for (int st = wp; st < 2 * KS; st += kTileBlocks) {
-                    const bool isk = st < KS;
-                    const int quad = (isk ? st : st - KS) * 4 + (lane >> 3);
-                    const int64_t words = isk ? kw : vw;
-                    const uint32_t* src = (isk ? Kp : Vp) + (int64_t)quad * 16 * words + i0 / 32 + 2 * b;
-                    uint2 W[4][4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) W[e][j] = __ldg(reinterpret_cast<const uint2*>(src + (e * 4 + j) * words));
-                    uint32_t N[4][2][4];                // [channel][word][r]
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        planes_to_nibbles(W[e][0].x, W[e][1].x, W[e][2].x, W[e][3].x, N[e][0]);
-                        planes_to_nibbles(W[e][0].y, W[e][1].y, W[e][2].y, W[e][3].y, N[e][1]);
-                    }
-                    if (isk) {
-                        uint4* dst = reinterpret_cast<uint4*>(s_k + b * Sh::kBlkWords + (quad >> 2) * 128) + (quad & 3);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-#pragma unroll
-                            for (int k4 = 0; k4 < 2; ++k4) {
-                                const uint32_t sel = k4 ? 0x7632u : 0x5410u;
-                                dst[(2 * r + k4) * 4] =
-                                    make_uint4(__byte_perm(N[0][0][r], N[1][0][r], sel), __byte_perm(N[0][1][r], N[1][1][r], sel),
-                                               __byte_perm(N[2][0][r], N[3][0][r], sel), __byte_perm(N[2][1][r], N[3][1][r], sel));
-                            }
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(s_v + b * Sh::kBlkWords + (quad >> 2) * 128) + (quad & 3) * 8;
-#pragma unroll
-                        for (int gi = 0; gi < 2; ++gi)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                dst[gi * 4 + r] = make_uint4(N[2 * gi][0][r], N[2 * gi + 1][0][r], N[2 * gi][1][r], N[2 * gi + 1][1][r]);
-                    }
-                }
-                for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
-                    const bool isk = c < D;
-                    const int ch = isk ? c : c - D;
-                    const uint16_t* src = isk ? Ks + (int64_t)ch * (kw / 2) : Vs + (int64_t)ch * (vw / 2);
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + i0 / kBlock));
-                    uint16_t* dst = (isk ? s_ks : s_vs) + ch;
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        dst[(2 * e) * D] = (uint16_t)w[e];
-                        dst[(2 * e + 1) * D] = (uint16_t)(w[e] >> 16);
-                    }
-                }
-            }
-            __syncthreads();
-            const int k0 = i0 + wp * kBlock;            // this warp's block
-            int most = 0;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) most = limit[nt] > most ? limit[nt] : most;
-            if (!__any_sync(0xffffffffu, k0 < most)) continue;
-
-            // ---- S = codes . Q'
-            const uint16_t* bs = s_ks + wp * D;
-            // the block's largest scale sets a power of two that keeps Q' inside fp16
-            float sc, back;   // back = 2^24 / sc
-            {
+                const uint32_t keep = act ? (k0 + kBlock < most ? 0xFFFFFFFFu : 0xFFFFu) : 0u;
                 __half2 mh = __float2half2_rn(0.0f);
+                stuck |= !barrier_wait(s_full + kRing, u & 1);
+                uint32_t sw[2 * D / 32];                // of two blocks: K's channels, then V's
 #pragma unroll
-                for (int e = 0; e < (D + 63) / 64; ++e)
-                    if (D >= 64 || lane < D / 2)
-                        mh = __hmax2(mh, *reinterpret_cast<const __half2*>(bs + 2 * lane + 64 * e));
-                float dm = fmaxf(__low2float(mh), __high2float(mh));
+                for (int i = 0; i < 2 * D / 32; ++i) sw[i] = reinterpret_cast<const uint32_t*>(s_rs)[(32 * i + lane) * (kTile / kBlock / 2) + (wp ^ (lane & 4))];
+                barrier_arrive(s_read + kRing);
 #pragma unroll
-                for (int o = 16; o; o >>= 1) dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, o));
-                // dm * sc in [2^12, 2^13); an f16 is at least 2^-24
-                const int ex = dm > 0.0f ? (int)(__float_as_uint(dm) >> 23) : 127;
-                sc = __uint_as_float((uint32_t)(266 - ex) << 23);
-                back = __uint_as_float((uint32_t)(ex + 12) << 23);
-            }
-            float S[NT][4][4], B15[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    B15[nt][e] = 0.0f;
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) S[nt][p][e] = 0.0f;
+                for (int i = 0; i < 2 * D / 32; ++i) {
+                    const uint32_t v = sw[i] & keep;
+                    if (i < D / 32) mh = __hmax2(mh, as_half2(v));
+                    uint16_t* dst = scales + (i < D / 32 ? 0 : 2 * D) + paired<CH>(32 * (i % (D / 32)) + lane);
+                    dst[0] = (uint16_t)v;
+                    dst[D] = (uint16_t)(v >> 16);
                 }
-            const uint32_t a15[4] = {0x000F000Fu, 0x000F000Fu, 0x000F000Fu, 0x000F000Fu};
-            const uint4* kc = reinterpret_cast<const uint4*>(s_k + wp * Sh::kBlkWords) + lane;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const uint4 raw = kc[ks * 32];
-                const uint2 d4 = *reinterpret_cast<const uint2*>(bs + 16 * ks + 4 * lt);
-                const float2 da = __half22float2(*reinterpret_cast<const __half2*>(&d4.x));
-                const float2 db = __half22float2(*reinterpret_cast<const __half2*>(&d4.y));
-                const float dl[4] = {da.x * sc, da.y * sc, db.x * sc, db.y * sc};
-                uint32_t bq[NT][2];
+                for (int o = 16; o; o >>= 1) {
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&mh), o);
+                    mh = __hmax2(mh, as_half2(other));
+                }
+                // a power of two sc keeps Q' inside fp16: the block's largest scale times it is
+                // in [2^6, 2^7) (or sc is 2^15, the largest factor in fp16: Q' then has 22 bits
+                // below its largest still)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float dm = b ? __high2float(mh) : __low2float(mh);
+                    const int ex = max((int)(__float_as_uint(dm) >> 23), 118);
+                    sc2[b] = __float2half2_rn(__uint_as_float((uint32_t)(260 - ex) << 23));
+                    back[b] = __uint_as_float((uint32_t)(ex + 18) << 23);   // 2^24 / sc
+                }
+            }
+            // scores of 16-key tiles p; then, in [p][0] and [p][1], the bits of their weights as operands
+            float S[2][NT][4][4], B15[2][NT][4], neg[2][NT];
+            const int pl = (lane & 7) + 8 * (lane >> 4), blk = (lane >> 3) & 1;   // the lane's channel pair and block
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float4 q4 = *reinterpret_cast<const float4*>(s_q + ((nt * KS + ks) * 4 + (lg >> 1)) * 16 + 4 * lt);
-                    const float v[4] = {q4.x * dl[0], q4.y * dl[1], q4.z * dl[2], q4.w * dl[3]};
-                    float z[4];
+                    neg[b][nt] = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float h = leading11(v[e]);
-                        z[e] = low ? v[e] - h : h;
+                        B15[b][nt][e] = 0.0f;
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) S[b][nt][p][e] = 0.0f;
                     }
-                    bq[nt][0] = half2_of(z[0], z[1]);
-                    bq[nt][1] = half2_of(z[2], z[3]);
-                    mma(B15[nt], a15, bq[nt]);
                 }
+#pragma unroll 1
+            for (int c = 0; c < 2 * NC; ++c, ++j) {
+                const bool isk = c < NC;
+                const int rj = j % kRing;
+                // ---- the chunk's planes of the warp's blocks to registers, as codes to the warp's own memory
+                stuck |= !barrier_wait(s_full + rj, (uint32_t)(j / kRing) & 1);
+                uint2 W[2][4];                          // [channel of the pair][plane]
+                const uint2* src = reinterpret_cast<const uint2*>(s_raw + rj * Sh::kRaw) + pl * 16 + (wp ^ (pl & 7)) * 2 + blk;
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    uint32_t a[4];
-                    operand(raw, p, a);
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma(S[nt][p], a, bq[nt]);
+                    for (int k = 0; k < 4; ++k) W[e][k] = src[(k * CH + e * HP) * 16];
+                // the last warp to have read a buffer has the next chunk copied into it
+                barrier_arrive(s_read + rj);
+                uint32_t N[2][2][4];                    // [channel][word][r]
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    planes_to_nibbles(W[e][0].x, W[e][1].x, W[e][2].x, W[e][3].x, N[e][0]);
+                    planes_to_nibbles(W[e][0].y, W[e][1].y, W[e][2].y, W[e][3].y, N[e][1]);
                 }
-            }
+                uint32_t* dst = codes + blk * (Sh::kCodes / 2) + (pl >> 3) * 128;
+                // both layouts keep the lanes of a write, and of a read, on different banks
+                if (isk) {
+                    // row g of the second block lies where row g ^ 1 would
+                    uint2* d2 = reinterpret_cast<uint2*>(dst) + (pl & 7);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int k4 = 0; k4 < 2; ++k4) {
+                            const uint32_t sel = k4 ? 0x7632u : 0x5410u;
+                            d2[(2 * r + (k4 ^ blk)) * 8] = make_uint2(__byte_perm(N[0][0][r], N[1][0][r], sel),
+                                                                      __byte_perm(N[0][1][r], N[1][1][r], sel));
+                        }
+                } else {
+                    // column pair t of row g lies where t ^ (g / 2) would
+                    uint4* d4 = reinterpret_cast<uint4*>(dst) + (pl & 7) * 4;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        d4[r ^ ((pl >> 1) & 3)] = make_uint4(N[0][0][r], N[1][0][r], N[0][1][r], N[1][1][r]);
+                }
+                // warps take turns at the copy of the buffer's next chunk, once every warp has read this one
+                if (wp == j % kWarps && j + kRing < chunks) {
+                    stuck |= !barrier_wait(s_read + rj, (uint32_t)(j / kRing) & 1);
+                    const int cn = c + kRing, un = u + cn / (2 * NC);
+                    if (lane == 0) {
+                        if (un < re) copy(rw, ub + un, cn % (2 * NC), rj);
+                        else copy(row_of(map, ub + un, Hkv, sets), ub + un, cn % (2 * NC), rj);
+                    }
+                }
+                if (c == 1 && wp == u % kWarps && u + 1 < units) {   // and at that of the next tile's scales
+                    stuck |= !barrier_wait(s_read + kRing, u & 1);
+                    if (lane == 0) copy_scale(u + 1 < re ? rw : row_of(map, ub + u + 1, Hkv, sets), ub + u + 1);
+                }
+                __syncwarp();
+                if (!act) continue;
+                if (isk) {
+                    // ---- S += codes . Q' of this chunk's channels
+                    const uint32_t a15[4] = {0x000F000Fu, 0x000F000Fu, 0x000F000Fu, 0x000F000Fu};
+                    const uint4* kc = reinterpret_cast<const uint4*>(codes);
+#pragma unroll
+                    for (int k = 0; k < CK; ++k) {
+                        const int ks = c * CK + k;
+                        uint32_t bq[2][NT][2];
+                        __half2 da[2], db[2];
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const uint2 d4 = *reinterpret_cast<const uint2*>(scales + b * D + 16 * ks + 4 * lt);
+                            da[b] = __hmul2(as_half2(d4.x), sc2[b]);
+                            db[b] = __hmul2(as_half2(d4.y), sc2[b]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint4 q4 = *reinterpret_cast<const uint4*>(s_q + ((nt * KS + ks) * 32 + lane) * 4);
+                            uint2 q2 = make_uint2(0u, 0u);
+                            if (F32) q2 = *reinterpret_cast<const uint2*>(s_q2 + ((nt * KS + ks) * 32 + lane) * 2);
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                // even column: z = rn(q1 d); odd: z = q1 d - rn(q1 d), exact, + q2 d
+                                __half2 za = __hfma2(as_half2(q4.z), da[b], __hmul2_rn(as_half2(q4.x), da[b]));
+                                __half2 zb = __hfma2(as_half2(q4.w), db[b], __hmul2_rn(as_half2(q4.y), db[b]));
+                                if (F32) {
+                                    za = __hfma2(as_half2(q2.x), da[b], za);
+                                    zb = __hfma2(as_half2(q2.y), db[b], zb);
+                                }
+                                bq[b][nt][0] = *reinterpret_cast<const uint32_t*>(&za);
+                                bq[b][nt][1] = *reinterpret_cast<const uint32_t*>(&zb);
+                                mma(B15[b][nt], a15, bq[b][nt]);
+                            }
+                        }
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const uint4 raw = kc[b * (Sh::kCodes / 8) + k * 32 + (lane ^ (b * 4))];
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                uint32_t a[4];
+                                operand(raw, p, a);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma(S[b][nt][p], a, bq[b][nt]);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (c < NC - 1) continue;
 
-            // ---- weights: lane (g, t) holds query t of the tile, 8 keys
-            uint32_t Pb[NT][4][2];
-            const bool cut = k0 + kBlock > least;       // some query of the set does not see the whole block
-            float shift[NT];
-            bool moved = false;
+                    // ---- weights: lane (g, t) holds query t of the tile, 8 keys of each block
+                    const bool cut = k0 + 2 * kBlock > least;   // some query of the set does not see all keys
+                    float shift[NT];
+                    bool moved = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float off = -0.5f * (B15[nt][0] + B15[nt][1]);
-                float mx = -INFINITY;
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float f = s_f[nt * kTilePairs + lt];
+                        float F[2];
+                        float mn = m[nt];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const float f = (p & 1) ? 0.0625f : 1.0f;
-                    S[nt][p][0] = fmaf(S[nt][p][0] + S[nt][p][1], f, off);
-                    S[nt][p][2] = fmaf(S[nt][p][2] + S[nt][p][3], f, off);
-                    if (cut) {
-                        const int key = k0 + 4 * (p + 4 * (lg & 1)) + (lg >> 1);
-                        if (key >= limit[nt]) S[nt][p][0] = -INFINITY;
-                        if (key + 32 >= limit[nt]) S[nt][p][2] = -INFINITY;
+                        for (int b = 0; b < 2; ++b) {
+                            const float off = -0.5f * (B15[b][nt][0] + B15[b][nt][1]);
+                            float mx = -INFINITY;
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                const float un = (p & 1) ? 0.0625f : 1.0f;
+                                float* v = S[b][nt][p];
+                                v[0] = fmaf(v[0] + v[1], un, off);
+                                v[2] = fmaf(v[2] + v[3], un, off);
+                                if (cut) {
+                                    const int key = k0 + b * kBlock + 4 * (p + 4 * (lg & 1)) + (lg >> 1);
+                                    if (key >= limit[nt]) v[0] = -INFINITY;
+                                    if (key + 32 >= limit[nt]) v[2] = -INFINITY;
+                                }
+                                mx = fmaxf(mx, fmaxf(v[0], v[2]));
+                            }
+                            F[b] = f * back[b];
+                            mn = fmaxf(mn, mx * F[b]);
+                        }
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                        const float base = mn == -INFINITY ? 0.0f : mn;
+                        // S F - base is rounded once; where the product's own rounding exceeds
+                        // the exponents that matter, both are rounded alike instead
+                        if (fabsf(base) > 1048576.0f) {
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                                for (int p = 0; p < 4; ++p) {
+                                    S[b][nt][p][0] *= F[b];
+                                    S[b][nt][p][2] *= F[b];
+                                }
+                                F[b] = 1.0f;
+                            }
+                        }
+                        shift[nt] = ex2(m[nt] - base);      // 0 while nothing has been seen
+                        moved |= mn != m[nt];
+                        m[nt] = mn;
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                // weights times 2^15, or 2^11 where the codes come 16 times as large
+                                const float up = (p & 1) ? 2048.0f : 32768.0f;
+#pragma unroll
+                                for (int w = 0; w < 2; ++w) {
+                                    const float v = ex2(fmaf(S[b][nt][p][2 * w], F[b], -base)) * up;
+                                    const float h = leading11(v);
+                                    S[b][nt][p][w] = __uint_as_float(transpose8x8(half2_of(h, v - h)));
+                                }
+                            }
                     }
-                    mx = fmaxf(mx, fmaxf(S[nt][p][0], S[nt][p][2]));
-                }
+                    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                float F = s_f[nt * kTilePairs + lt] * back;
-                const float mn = fmaxf(m[nt], mx * F);
-                const float base = mn == -INFINITY ? 0.0f : mn;
-                // S F - base is rounded once; where the product's own rounding exceeds
-                // the exponents that matter, both are rounded alike instead
-                if (fabsf(base) > 1048576.0f) {
+                        for (int nt = 0; nt < NT; ++nt) {
+                            l[nt] *= shift[nt];
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        S[nt][p][0] *= F;
-                        S[nt][p][2] *= F;
+                            for (int mt = 0; mt < KS; ++mt) {
+                                O[nt][mt][0] *= shift[nt];
+                                O[nt][mt][1] *= shift[nt];
+                            }
+                        }
                     }
-                    F = 1.0f;
-                }
-                shift[nt] = ex2(m[nt] - base);          // 0 while nothing has been seen
-                moved |= mn != m[nt];
-                m[nt] = mn;
+                    // ---- 15 sum P: the offset of the codes, and the weights' sum
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    // weights times 2^15, or 2^11 where the codes come 16 times as large
-                    const float up = (p & 1) ? 2048.0f : 32768.0f;
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const float v = ex2(fmaf(S[nt][p][2 * w], F, -base)) * up;
-                        const float h = leading11(v);
-                        Pb[nt][p][w] = transpose8x8(half2_of(h, v - h));
-                    }
-                }
-            }
-            if (__any_sync(0xffffffffu, moved)) {
+                        for (int b = 0; b < 2; ++b) {
+                            float c4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    l[nt] *= shift[nt];
+                            for (int p = 0; p < 4; ++p) {
+                                uint32_t a[4];
+                                operand(make_uint4(~0u, ~0u, ~0u, ~0u), p, a);
+                                mma_p(c4, a, S[b][nt][p]);
+                            }
+                            const float sum = c4[0] + c4[1];
+                            neg[b][nt] = -0.5f * sum;
+                            l[nt] = fmaf(sum, 512.0f / 15.0f, l[nt]);   // 2^24 / 2^15
+                        }
+                } else {
+                    // ---- O += Delta (codes - 7.5) . P; the chunk's outputs are registers, so each chunk has its own code
+                    const uint4* vc = reinterpret_cast<const uint4*>(codes) + (lane ^ ((lane >> 3) & 3));
 #pragma unroll
-                    for (int mt = 0; mt < KS; ++mt) {
-                        O[nt][mt][0] *= shift[nt];
-                        O[nt][mt][1] *= shift[nt];
-                    }
-                }
-            }
-            // ---- 15 sum P: the offset of the codes, and the weights' sum
-            float neg[NT];
+                    for (int cv = 0; cv < NC; ++cv)
+                        if (c == NC + cv) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int k = 0; k < CK; ++k) {
+                            const int mt = cv * CK + k;
+                            float acc[2][NT][4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    uint32_t a[4];
-                    operand(make_uint4(~0u, ~0u, ~0u, ~0u), p, a);
-                    mma(c, a, Pb[nt][p]);
-                }
-                const float sum = c[0] + c[1];
-                neg[nt] = -0.5f * sum;
-                l[nt] = fmaf(sum, 512.0f / 15.0f, l[nt]);   // 2^24 / 2^15
-            }
-            // ---- O += Delta (codes - 7.5) . P
-            const uint4* vc = reinterpret_cast<const uint4*>(s_v + wp * Sh::kBlkWords) + lane;
-            const uint16_t* vs = s_vs + wp * D + 2 * lg;
+                            for (int b = 0; b < 2; ++b) {
+                                const uint4 raw = vc[b * (Sh::kCodes / 8) + k * 32];
 #pragma unroll
-            for (int mt = 0; mt < KS; ++mt) {
-                const uint4 raw = vc[mt * 32];
-                const float2 dv = __half22float2(*reinterpret_cast<const __half2*>(vs + 16 * mt));
-                float c[NT][4];
+                                for (int nt = 0; nt < NT; ++nt) acc[b][nt][0] = acc[b][nt][2] = neg[b][nt], acc[b][nt][1] = acc[b][nt][3] = 0.0f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][2] = neg[nt], c[nt][1] = c[nt][3] = 0.0f;
+                                for (int p = 0; p < 4; ++p) {
+                                    uint32_t a[4];
+                                    operand(raw, p, a);
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    uint32_t a[4];
-                    operand(raw, p, a);
+                                    for (int nt = 0; nt < NT; ++nt) mma_p(acc[b][nt], a, S[b][nt][p]);
+                                }
+                            }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma(c[nt], a, Pb[nt][p]);
-                }
+                            for (int b = 0; b < 2; ++b) {
+                                const float2 dv = __half22float2(*reinterpret_cast<const __half2*>(scales + (2 + b) * D + 16 * mt + 2 * lg));
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    O[nt][mt][0] = fmaf(c[nt][0] + c[nt][1], dv.x, O[nt][mt][0]);
-                    O[nt][mt][1] = fmaf(c[nt][2] + c[nt][3], dv.y, O[nt][mt][1]);
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    O[nt][mt][0] = fmaf(acc[b][nt][0] + acc[b][nt][1], dv.x, O[nt][mt][0]);
+                                    O[nt][mt][1] = fmaf(acc[b][nt][2] + acc[b][nt][3], dv.y, O[nt][mt][1]);
+                                }
+                            }
+                        }
+                        }
+                    __syncwarp();
                 }
             }
         }
 
-        // ---- the warps' partials: merged here, o in units of 2^-9
-        __syncthreads();
-        float* s_o = reinterpret_cast<float*>(smem);    // [warp][pair][D]
+        // ---- the warps' partials: merged here, o in units of 2^-9; a warp's codes make room
+        __syncwarp();
+        float* s_o = reinterpret_cast<float*>(codes);   // [pair][D], channels pair by pair
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int x = nt * kTilePairs + lt;
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt)
-                *reinterpret_cast<float2*>(s_o + (wp * kPairs + x) * D + 16 * mt + 2 * lg) = make_float2(O[nt][mt][0], O[nt][mt][1]);
+                *reinterpret_cast<float2*>(s_o + x * D + 16 * mt + 2 * lg) = make_float2(O[nt][mt][0], O[nt][mt][1]);
             if (lg == 0) {
                 s_m[wp * kPairs + x] = m[nt];
                 s_l[wp * kPairs + x] = l[nt];
             }
         }
         __syncthreads();
-        float* slot = slots + (blockIdx.x + row) * (kPairs * (D + 2));
+        float* part = slots + (int64_t)(blockIdx.x + rw.row) * (kPairs * (D + 2));
         for (int e = threadIdx.x; e < kPairs * D; e += kThreads) {
-            const int x = e / D, c = e % D, pr = set * kPairs + x;
+            const int x = e / D, c = e % D, pr = rw.set * kPairs + x;
             float M = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kTileBlocks; ++w) M = fmaxf(M, s_m[w * kPairs + x]);
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kPairs + x]);
             const float Mb = M == -INFINITY ? 0.0f : M;
             float L = 0.0f, o = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kTileBlocks; ++w) {
+            for (int w = 0; w < kWarps; ++w) {
                 const float f = ex2(s_m[w * kPairs + x] - Mb);
                 L = fmaf(s_l[w * kPairs + x], f, L);
-                o = fmaf(s_o[(w * kPairs + x) * D + c], f, o);
+                o = fmaf(reinterpret_cast<const float*>(s_codes + w * Sh::kOwn)[x * D + paired<CH>(c)], f, o);
             }
             o *= 512.0f;
             if (!whole) {
-                slot[e] = o;
-                if (c == 0) slot[kPairs * D + x] = M, slot[kPairs * (D + 1) + x] = L;
+                part[e] = o;
+                if (c == 0) part[kPairs * D + x] = M, part[kPairs * (D + 1) + x] = L;
             } else if (pr < C) {
-                const int64_t h = ((int64_t)s * T + pr / G) * Hq + g * G + pr % G;
+                const int64_t h = ((int64_t)s * T + pr / G) * Hq + rw.g * G + pr % G;
                 if (parts) {
                     parts[h * (D + 2) + c] = o;
                     if (c == 0) parts[h * (D + 2) + D] = M, parts[h * (D + 2) + D + 1] = L;
@@ -472,7 +669,10 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
                 }
             }
         }
+        __syncthreads();                                // before the next row's queries and codes
+        if (u < units) rw = row_of(map, ub + u, Hkv, sets);
     }
+    if (stuck && lane == 0) atomicOr(status, (unsigned)FATHOM_DEV_TIMEOUT);
 }
 
 // One CTA per (row, pair) whose keys were shared by several CTAs, or that has
@@ -480,28 +680,25 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
 constexpr int kMergeThreads = 256;
 __global__ void __launch_bounds__(kMergeThreads)
 store_attend_merge_kernel(const __grid_constant__ AttendMap map, const float* __restrict__ slots, int T, int Hq, int Hkv,
-                          int sets, int pairs, int D, int P, float* __restrict__ out, float* __restrict__ parts) {
+                          int sets, int pairs, int D, float* __restrict__ out, float* __restrict__ parts) {
     __shared__ float s_w[kMaxCtas];
     __shared__ float s_red[2][kMergeThreads / 32];
     __shared__ float4 s_o[kMergeThreads];
     pdl_wait();
     const int G = Hq / Hkv, C = T * G;
-    const int64_t row = blockIdx.x / pairs;
-    const int x = blockIdx.x % pairs;
-    const int s = (int)(row / (Hkv * sets)), rl = (int)(row % (Hkv * sets));
+    const int row = blockIdx.x / pairs, x = blockIdx.x % pairs;
+    const int s = row / (Hkv * sets), rl = row % (Hkv * sets);
     const int g = rl / sets, pr = rl % sets * pairs + x;
     if (pr >= C) return;
-    const int64_t U = map.unit0[map.nsess];
-    const int64_t ub = map.unit0[s] + (int64_t)rl * map.tiles[s], ue = ub + map.tiles[s];
-    int64_t p0 = 0;
-    int np = 0;
+    const int ub = map.unit0[s] + rl * map.tiles[s], ue = ub + map.tiles[s];
+    int p0 = 0, np = 0;
     if (ue > ub) {
-        p0 = run_of(ub, U, P);
-        np = (int)(run_of(ue - 1, U, P) - p0) + 1;
+        p0 = run_of(map, ub);
+        np = run_of(map, ue - 1) - p0 + 1;
         if (np == 1) return;                     // written by its CTA
     }
     const int64_t st = (int64_t)pairs * (D + 2);
-    const float* base = slots + (p0 + row) * st;
+    const float* base = slots + (int64_t)(p0 + row) * st;
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     float M = -INFINITY;
     for (int p = threadIdx.x; p < np; p += kMergeThreads) {
@@ -559,8 +756,8 @@ store_attend_merge_kernel(const __grid_constant__ AttendMap map, const float* __
     }
 }
 
-// 8-column tiles of a set: as many as the pairs fill, up to four (16 pairs)
-inline int tiles_of_set(int64_t C) { return C <= kTilePairs ? 1 : (C <= 2 * kTilePairs ? 2 : 4); }
+// 8-column tiles of a set: one or two (8 pairs)
+inline int tiles_of_set(int64_t C) { return C <= kTilePairs ? 1 : 2; }
 
 }  // namespace
 
@@ -573,25 +770,84 @@ size_t store_attend_workspace_bytes(int S, int T, int Hq, int Hkv, int d) {
 
 namespace {
 
-template <int D, int NT>
-cudaError_t launch_tiles(const AttendMap& map, int P0, const void* q, int q_dtype, int T, int Hq, int Hkv, int sets,
-                         float* slots, float* out, float* parts, cudaStream_t stream, int* P) {
-    using Sh = Shape<D, NT>;
-    static_assert(Sh::kSmem * Sh::kCtasPerSm <= kMaxSmem, "the CTAs of an SM fit");
-    auto kern = store_attend_kernel<D, NT>;
+struct Call {
+    AttendMap& map;
+    const void* q;
+    int q_dtype, T, Hq, Hkv, sets;
+    float *slots, *out, *parts;
+    cudaStream_t stream;
+    bool shared;   // some row's keys may be shared by several CTAs, or a row has none
+    int P;
+};
+
+// The tensor maps of a store: planes as words, channels of all heads, planes, a box
+// being a tile's 128 bytes of a chunk's channels and all planes, 16-byte pieces
+// of each row swizzled by the row number; scales as blocks, channels of all
+// heads, a box being a tile's blocks of a head's channels.
+bool tensor_maps(CUtensorMap* tm, CUtensorMap* stm, const uint32_t* planes, const uint16_t* scales, int channels, int d,
+                 int64_t n_pad) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return false;
+    const cuuint64_t row = (cuuint64_t)(n_pad / 8);
+    const cuuint64_t dims[3] = {row / 4, (cuuint64_t)channels, 4}, strides[2] = {4 * row, row};
+    const cuuint32_t box[3] = {kTile / 32, 32, 4}, step[3] = {1, 1, 1};
+    const cuuint64_t sdims[2] = {(cuuint64_t)(n_pad / kBlock), (cuuint64_t)channels}, sstrides[1] = {(cuuint64_t)(n_pad / kBlock) * 2};
+    const cuuint32_t sbox[2] = {kTile / kBlock, (cuuint32_t)d};
+    return encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint32_t*>(planes), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+           encode(stm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint16_t*>(scales), sdims, sstrides, sbox, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch_type(Call& a) {
+    using Sh = Shape<D, NT, F32>;
+    static_assert(Sh::kCtas * (Sh::kSmem + 1024) <= kMaxSmem + 1024, "the CTAs of an SM fit");
+    int64_t U = 0;
+    for (int s = 0; s < a.map.nsess; ++s) {
+        const int64_t last = a.map.visible[s] + a.T - 1;   // keys that the last token sees
+        const int64_t keys = last < a.map.n[s] ? (last > 0 ? last : 0) : a.map.n[s];
+        if (U > INT32_MAX / 16) return cudaErrorInvalidValue;   // unit and chunk numbers are 32 bits
+        a.map.unit0[s] = (int)U;
+        a.map.tiles[s] = (int)((keys + kTile - 1) / kTile);
+        U += (int64_t)a.map.tiles[s] * a.Hkv * a.sets;
+        a.shared = a.shared || a.map.tiles[s] != 1;
+    }
+    if (U > INT32_MAX / 16) return cudaErrorInvalidValue;
+    a.map.unit0[a.map.nsess] = (int)U;
+    if (U == 0) return cudaSuccess;
+    a.P = (int)(U < 148 * Sh::kCtas ? U : 148 * Sh::kCtas);
+    a.map.each = (int)(U / a.P);
+    a.map.more = (int)(U % a.P);
+    for (int s = 0; s < a.map.nsess; ++s)
+        if (!tensor_maps(&a.map.k_tm[s], &a.map.ks_tm[s], a.map.k_planes[s], a.map.k_scales[s], a.Hkv * D, D, a.map.k_pad[s]) ||
+            !tensor_maps(&a.map.v_tm[s], &a.map.vs_tm[s], a.map.v_planes[s], a.map.v_scales[s], a.Hkv * D, D, a.map.v_pad[s]))
+            return cudaErrorInvalidValue;
+    auto kern = store_attend_kernel<D, NT, F32>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
     if (e != cudaSuccess) return e;
-    *P = P0 < 148 * Sh::kCtasPerSm ? P0 : 148 * Sh::kCtasPerSm;
-    return launch_ex(kern, dim3(*P), dim3(kThreads), Sh::kSmem, stream, false, 1, map, q, q_dtype, T, Hq, Hkv, sets,
-                     slots, out, parts);
+    return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, false, 1, a.map, a.q, a.q_dtype, a.T,
+                     a.Hq, a.Hkv, a.sets, a.slots, a.out, a.parts, device_status_ptr());
+}
+
+template <int D, int NT>
+cudaError_t launch_tiles(Call& a) {
+    return a.q_dtype == FATHOM_F32 ? launch_type<D, NT, true>(a) : launch_type<D, NT, false>(a);
 }
 
 template <int D>
-cudaError_t launch_dim(int nt, const AttendMap& map, int P0, const void* q, int q_dtype, int T, int Hq, int Hkv, int sets,
-                       float* slots, float* out, float* parts, cudaStream_t stream, int* P) {
-    if (nt == 1) return launch_tiles<D, 1>(map, P0, q, q_dtype, T, Hq, Hkv, sets, slots, out, parts, stream, P);
-    if (nt == 2) return launch_tiles<D, 2>(map, P0, q, q_dtype, T, Hq, Hkv, sets, slots, out, parts, stream, P);
-    return launch_tiles<D, 4>(map, P0, q, q_dtype, T, Hq, Hkv, sets, slots, out, parts, stream, P);
+cudaError_t launch_dim(int nt, Call& a) {
+    return nt == 1 ? launch_tiles<D, 1>(a) : launch_tiles<D, 2>(a);
 }
 
 }  // namespace
@@ -600,34 +856,18 @@ cudaError_t launch_store_attend(AttendMap& map, int Hkv, int d, const void* q, i
                                 float* parts, void* ws, cudaStream_t stream) {
     const int64_t C = (int64_t)T * (Hq / Hkv);
     const int nt = tiles_of_set(C), pairs = nt * kTilePairs;
-    const int sets = (int)((C + pairs - 1) / pairs);
-    int64_t U = 0;
-    bool shared = false;   // some row's keys may be shared by several CTAs, or a row has none
-    for (int s = 0; s < map.nsess; ++s) {
-        const int64_t last = map.visible[s] + T - 1;   // keys that the last token sees
-        const int64_t keys = last < map.n[s] ? (last > 0 ? last : 0) : map.n[s];
-        map.unit0[s] = U;
-        map.tiles[s] = (int)((keys + kTile - 1) / kTile);
-        U += (int64_t)map.tiles[s] * Hkv * sets;
-        shared = shared || map.tiles[s] != 1;
+    Call a{map, q, q_dtype, T, Hq, Hkv, (int)((C + pairs - 1) / pairs), static_cast<float*>(ws), out, parts, stream, false, 0};
+    cudaError_t e;
+    switch (d) {
+        case 32: e = launch_dim<32>(nt, a); break;
+        case 64: e = launch_dim<64>(nt, a); break;
+        case 128: e = launch_dim<128>(nt, a); break;
+        case 256: e = launch_dim<256>(nt, a); break;
+        default: return cudaErrorInvalidValue;
     }
-    map.unit0[map.nsess] = U;
-    float* slots = static_cast<float*>(ws);
-    int P = 0;
-    if (U > 0) {
-        const int P0 = (int)(U < kMaxCtas ? U : kMaxCtas);
-        cudaError_t e;
-        switch (d) {
-            case 32: e = launch_dim<32>(nt, map, P0, q, q_dtype, T, Hq, Hkv, sets, slots, out, parts, stream, &P); break;
-            case 64: e = launch_dim<64>(nt, map, P0, q, q_dtype, T, Hq, Hkv, sets, slots, out, parts, stream, &P); break;
-            case 128: e = launch_dim<128>(nt, map, P0, q, q_dtype, T, Hq, Hkv, sets, slots, out, parts, stream, &P); break;
-            case 256: e = launch_dim<256>(nt, map, P0, q, q_dtype, T, Hq, Hkv, sets, slots, out, parts, stream, &P); break;
-            default: return cudaErrorInvalidValue;
-        }
-        if (e != cudaSuccess || !shared) return e;
-    }
-    return launch_ex(store_attend_merge_kernel, dim3((unsigned)((int64_t)map.nsess * Hkv * sets * pairs)),
-                     dim3(kMergeThreads), 0, stream, U > 0, 1, map, slots, T, Hq, Hkv, sets, pairs, d, P, out, parts);
+    if (e != cudaSuccess || !a.shared) return e;
+    return launch_ex(store_attend_merge_kernel, dim3((unsigned)((int64_t)map.nsess * Hkv * a.sets * pairs)),
+                     dim3(kMergeThreads), 0, stream, a.P > 0, 1, map, a.slots, T, Hq, Hkv, a.sets, pairs, d, out, parts);
 }
 
 }  // namespace fathom

@@ -80,7 +80,8 @@ typedef enum { FATHOM_F32 = 0, FATHOM_BF16 = 1 } fathom_dtype;
 enum {
     FATHOM_DEV_BAD_DEPTH = 1u << 0,   /* a depth above 4 was read; that channel was skipped */
     FATHOM_DEV_BAD_INDEX = 1u << 1,   /* an index outside [0,n) reached sparse attention; skipped */
-    FATHOM_DEV_TOPK_OVERFLOW = 1u << 2 /* internal: a top-k buffer overflowed (never expected) */
+    FATHOM_DEV_TOPK_OVERFLOW = 1u << 2, /* internal: a top-k buffer overflowed (never expected) */
+    FATHOM_DEV_TIMEOUT = 1u << 3 /* internal: a bounded wait inside a kernel gave up (never expected) */
 };
 
 /*
