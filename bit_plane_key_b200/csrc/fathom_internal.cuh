@@ -1,7 +1,6 @@
 // Internal declarations shared by the CUDA translation units of libfathom.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -204,12 +203,9 @@ cudaError_t launch_append_rows(const uint16_t* K_rows, uint32_t* k_planes, uint1
                                int d, int64_t rows_n, int64_t row_stride, int64_t blk0, int64_t n, cudaStream_t stream);
 
 // Sessions of an attention over stores: query token t of session s sees the
-// keys below min(n[s], visible[s] + t).  launch_store_attend fills tiles (per
-// row of session s) and unit0 (prefix sums over the sessions' rows).
-constexpr int kAttendSets = 32;   // sessions of a launch
+// keys below min(n[s], visible[s] + t).
+constexpr int kAttendSets = 32;   // sessions of a launch (their tensor maps are its parameters)
 struct AttendMap {
-    // planes and scales of K and V, made by launch_store_attend
-    alignas(64) CUtensorMap k_tm[kAttendSets], ks_tm[kAttendSets], v_tm[kAttendSets], vs_tm[kAttendSets];
     int nsess;
     const uint32_t* k_planes[kAttendSets];
     const uint16_t* k_scales[kAttendSets];
@@ -219,13 +215,10 @@ struct AttendMap {
     int64_t v_pad[kAttendSets];
     int64_t n[kAttendSets];
     int64_t visible[kAttendSets];
-    int tiles[kAttendSets];
-    int unit0[kAttendSets + 1];
-    int each, more;   // units of a CTA, and CTAs with one more
 };
 size_t store_attend_workspace_bytes(int S, int T, int Hq, int Hkv, int d);
 // parts non-null: per-row partials [S][T][Hq][d + 2] instead of out
-cudaError_t launch_store_attend(AttendMap& map, int Hkv, int d, const void* q, int q_dtype, int T, int Hq, float* out,
+cudaError_t launch_store_attend(const AttendMap& map, int Hkv, int d, const void* q, int q_dtype, int T, int Hq, float* out,
                                 float* parts, void* ws, cudaStream_t stream);
 
 cudaError_t launch_probe(const void* src, size_t bytes, unsigned long long* sink, int ctas,

@@ -29,6 +29,8 @@
 // bits: the products lose no more than fp32 arithmetic would.  Scores never
 // leave the warp: a transposing move of 8x8 matrices makes the P operand of
 // the S accumulators.
+#include <cuda.h>
+
 #include "fathom_internal.cuh"
 
 namespace fathom {
@@ -69,21 +71,33 @@ __device__ __forceinline__ int paired(int c) {
     return c - l + 2 * (l % (CH / 2)) + l / (CH / 2);
 }
 
-// units are cut into runs: the first `more` of U / P + 1, the others of U / P = each
-__device__ __forceinline__ int run_start(const AttendMap& m, int p) { return p * m.each + (p < m.more ? p : m.more); }
-__device__ __forceinline__ int run_of(const AttendMap& m, int u) {
+// What the kernels know of the sessions of a launch, up to S of them: the part that
+// every warp reads first, then the tensor maps of planes and scales.  One session
+// has a type of its own: a launch copies its parameters, and reads them cold.
+struct Span {
+    int n, visible;     // query token t sees the keys below min(n, visible + t)
+    int unit0, tiles;   // its first unit; tiles of a row
+};
+template <int S>
+struct Spans {
+    int nsess;
+    int each, more;     // units of a CTA, and CTAs with one more
+    int pad;
+    Span span[S];
+};
+template <int S>
+struct Sessions {
+    Spans<S> at;
+    alignas(64) CUtensorMap k[S], ks[S], v[S], vs[S];
+};
+
+// units are cut into runs: the first `more` of each + 1, the others of each
+template <class M>
+__device__ __forceinline__ int run_start(const M& m, int p) { return p * m.each + (p < m.more ? p : m.more); }
+template <class M>
+__device__ __forceinline__ int run_of(const M& m, int u) {
     const int big = m.more * (m.each + 1);
     return u < big ? u / (m.each + 1) : m.more + (u - big) / m.each;
-}
-
-__device__ __forceinline__ int session_of_unit(const AttendMap& m, int u) {
-    int lo = 0, hi = m.nsess;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (m.unit0[mid] <= u) lo = mid;
-        else hi = mid;
-    }
-    return lo;
 }
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, const uint32_t* b) {
@@ -180,14 +194,19 @@ __device__ __forceinline__ void planes_to_nibbles(uint32_t w0, uint32_t w1, uint
     N[3] = pick(O, H >> 2, 0xCCCCCCCCu);
 }
 
-// operand value pairs p = 0..3 of a word of codes (odd p: 16 times the code)
-__device__ __forceinline__ void operand(const uint4& raw, int p, uint32_t* a) {
-    const uint32_t mask = (p & 1) ? 0x00F000F0u : 0x000F000Fu;
-    const int sh = (p & 2) ? 8 : 0;
-    a[0] = (raw.x >> sh) & mask;
-    a[1] = (raw.y >> sh) & mask;
-    a[2] = (raw.z >> sh) & mask;
-    a[3] = (raw.w >> sh) & mask;
+// operand value pairs p = 0..3 of a word of codes (odd p: 16 times the code).  The
+// last two are bytes 1 and 3 as they are less their upper nibbles: an exact
+// subtraction of subnormals, on another pipe than the ANDs
+__device__ __forceinline__ void operands(const uint4& raw, uint32_t a[4][4]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        a[0][e] = w[e] & 0x000F000Fu;
+        a[1][e] = w[e] & 0x00F000F0u;
+        const uint32_t y = __byte_perm(w[e], 0u, 0x4341);
+        a[3][e] = y & 0x00F000F0u;
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(a[2][e]) : "r"(y), "r"(a[3][e]));
+    }
 }
 
 // Where the keys of a block lie in the operands: key 32 w + 4 (p + 4 k4) + r is
@@ -204,22 +223,29 @@ struct Row {
     int s, g, set, row;
     int u0, u1;   // its units
 };
-__device__ __noinline__ Row row_of(const AttendMap& map, int u, int Hkv, int sets) {
+template <int S>
+__device__ __noinline__ Row row_of(const Spans<S>& m, int u, int Hkv, int sets) {
+    int lo = 0, hi = m.nsess;   // the last session that starts at or before u: empty ones start where the next does
+    while (S > 1 && hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (m.span[mid].unit0 <= u) lo = mid;
+        else hi = mid;
+    }
+    const Span& sp = m.span[lo];
     Row r;
-    r.s = session_of_unit(map, u);
-    const int tiles = map.tiles[r.s];
-    const int rl = (u - map.unit0[r.s]) / tiles;
+    r.s = lo;
+    const int rl = (u - sp.unit0) / sp.tiles;
     r.g = rl / sets;
     r.set = rl - r.g * sets;
-    r.row = r.s * Hkv * sets + rl;
-    r.u0 = map.unit0[r.s] + rl * tiles;
-    r.u1 = r.u0 + tiles;
+    r.row = lo * Hkv * sets + rl;
+    r.u0 = sp.unit0 + rl * sp.tiles;
+    r.u1 = r.u0 + sp.tiles;
     return r;
 }
 
-template <int D, int NT, bool F32>
+template <int D, int NT, bool F32, int NS>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT, F32>::kCtas)
-store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restrict__ q, int q_dtype, int T, int Hq,
+store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __restrict__ q, int q_dtype, int T, int Hq,
                     int Hkv, int sets, float* __restrict__ slots, float* __restrict__ out, float* __restrict__ parts,
                     unsigned int* status) {
     using Sh = Shape<D, NT, F32>;
@@ -238,8 +264,8 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
     uint64_t* s_full = reinterpret_cast<uint64_t*>(s_f + kPairs);   // [ring] the chunk has arrived; then the scales
     uint64_t* s_read = s_full + kRing + 1;              // every warp has read it
 
-    const int ub = run_start(map, blockIdx.x);
-    const int units = run_start(map, blockIdx.x + 1) - ub, chunks = units * (2 * NC);
+    const int ub = run_start(map.at, blockIdx.x);
+    const int units = run_start(map.at, blockIdx.x + 1) - ub, chunks = units * (2 * NC);
     const int G = Hq / Hkv, C = T * G;
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int lg = lane >> 2, lt = lane & 3;            // g and t of the operand layouts
@@ -247,16 +273,16 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
     // copies chunk c of a unit (NC chunks of K, then NC of V) of row r to ring buffer i
     auto copy = [&](const Row& r, int unit, int c, int i) {
         barrier_expect(s_full + i, 4 * Sh::kRaw);
-        copy_planes(s_raw + i * Sh::kRaw, c < NC ? &map.k_tm[r.s] : &map.v_tm[r.s], (unit - r.u0) * (kTile / 32),
+        copy_planes(s_raw + i * Sh::kRaw, c < NC ? &map.k[r.s] : &map.v[r.s], (unit - r.u0) * (kTile / 32),
                     r.g * D + (c < NC ? c : c - NC) * CH, s_full + i);
     };
     auto copy_scale = [&](const Row& r, int unit) {
         const int b = (unit - r.u0) * (kTile / kBlock);
         barrier_expect(s_full + kRing, 2 * 2 * Sh::kRawScales);
-        copy_scales(s_rs, &map.ks_tm[r.s], b, r.g * D, s_full + kRing);
-        copy_scales(s_rs + Sh::kRawScales, &map.vs_tm[r.s], b, r.g * D, s_full + kRing);
+        copy_scales(s_rs, &map.ks[r.s], b, r.g * D, s_full + kRing);
+        copy_scales(s_rs + Sh::kRawScales, &map.vs[r.s], b, r.g * D, s_full + kRing);
     };
-    Row rw = row_of(map, ub, Hkv, sets);
+    Row rw = row_of(map.at, ub, Hkv, sets);
     if (threadIdx.x == kThreads - 32) {                 // the first queries go to other warps
         for (int i = 0; i <= kRing; ++i) {
             barrier_init(s_full + i, 1);
@@ -266,7 +292,7 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
         copy_scale(rw, ub);
         for (int i = 0; i < kRing && i < chunks; ++i) {
             const int unit = ub + i / (2 * NC);
-            copy(unit < rw.u1 ? rw : row_of(map, unit, Hkv, sets), unit, i % (2 * NC), i);
+            copy(unit < rw.u1 ? rw : row_of(map.at, unit, Hkv, sets), unit, i % (2 * NC), i);
         }
     }
 
@@ -278,7 +304,7 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
         const int s = rw.s;
         const int left = rw.u1 - ub, re = left < units ? left : units;
         const bool whole = ub + u == rw.u0 && left <= units;   // no other CTA has a share of this row
-        const int n = (int)map.n[s];
+        const int n = map.at.span[s].n, visible = map.at.span[s].visible;
 
         // the set's queries in fp16, each scaled by a power of two to at most 2^6 to 2^7
         // in magnitude (so that the least fp16 is 2^-31 of it): q1 = the value's first
@@ -322,22 +348,18 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
         }
 
         float O[NT][KS][2], m[NT], l[NT];
-        int limit[NT], least = n, most;
+        int limit[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt] = -INFINITY;
             l[nt] = 0.0f;
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt) O[nt][mt][0] = O[nt][mt][1] = 0.0f;
-            const int64_t see = map.visible[s] + (rw.set * kPairs + nt * kTilePairs + lt) / G;
-            limit[nt] = (int)(see < n ? (see > 0 ? see : 0) : n);
+            limit[nt] = min(max(visible + (rw.set * kPairs + nt * kTilePairs + lt) / G, 0), n);
         }
-        {   // the set's first pair sees the fewest keys, its last the most
-            int64_t see = map.visible[s] + rw.set * kPairs / G;
-            if (see < n) least = (int)(see > 0 ? see : 0);
-            see = map.visible[s] + (rw.set * kPairs + kPairs - 1) / G;
-            most = (int)(see < n ? (see > 0 ? see : 0) : n);
-        }
+        // the set's first pair sees the fewest keys, its last the most
+        const int least = min(max(visible + rw.set * kPairs / G, 0), n);
+        const int most = min(max(visible + (rw.set * kPairs + kPairs - 1) / G, 0), n);
         __syncthreads();                                // the queries are in place
 
         for (; u < re; ++u) {
@@ -440,12 +462,12 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
                     const int cn = c + kRing, un = u + cn / (2 * NC);
                     if (lane == 0) {
                         if (un < re) copy(rw, ub + un, cn % (2 * NC), rj);
-                        else copy(row_of(map, ub + un, Hkv, sets), ub + un, cn % (2 * NC), rj);
+                        else copy(row_of(map.at, ub + un, Hkv, sets), ub + un, cn % (2 * NC), rj);
                     }
                 }
                 if (c == 1 && wp == u % kWarps && u + 1 < units) {   // and at that of the next tile's scales
                     stuck |= !barrier_wait(s_read + kRing, u & 1);
-                    if (lane == 0) copy_scale(u + 1 < re ? rw : row_of(map, ub + u + 1, Hkv, sets), ub + u + 1);
+                    if (lane == 0) copy_scale(u + 1 < re ? rw : row_of(map.at, ub + u + 1, Hkv, sets), ub + u + 1);
                 }
                 __syncwarp();
                 if (!act) continue;
@@ -485,14 +507,12 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
                         }
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
-                            const uint4 raw = kc[b * (Sh::kCodes / 8) + k * 32 + (lane ^ (b * 4))];
+                            uint32_t a[4][4];
+                            operands(kc[b * (Sh::kCodes / 8) + k * 32 + (lane ^ (b * 4))], a);
 #pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                uint32_t a[4];
-                                operand(raw, p, a);
+                            for (int p = 0; p < 4; ++p)
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) mma(S[b][nt][p], a, bq[b][nt]);
-                            }
+                                for (int nt = 0; nt < NT; ++nt) mma(S[b][nt][p], a[p], bq[b][nt]);
                         }
                     }
                     __syncwarp();
@@ -579,8 +599,7 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
                             float c4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                             for (int p = 0; p < 4; ++p) {
-                                uint32_t a[4];
-                                operand(make_uint4(~0u, ~0u, ~0u, ~0u), p, a);
+                                const uint32_t v15 = (p & 1) ? 0x00F000F0u : 0x000F000Fu, a[4] = {v15, v15, v15, v15};
                                 mma_p(c4, a, S[b][nt][p]);
                             }
                             const float sum = c4[0] + c4[1];
@@ -599,16 +618,14 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
                             float acc[2][NT][4];
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
-                                const uint4 raw = vc[b * (Sh::kCodes / 8) + k * 32];
+                                uint32_t a[4][4];
+                                operands(vc[b * (Sh::kCodes / 8) + k * 32], a);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) acc[b][nt][0] = acc[b][nt][2] = neg[b][nt], acc[b][nt][1] = acc[b][nt][3] = 0.0f;
 #pragma unroll
-                                for (int p = 0; p < 4; ++p) {
-                                    uint32_t a[4];
-                                    operand(raw, p, a);
+                                for (int p = 0; p < 4; ++p)
 #pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) mma_p(acc[b][nt], a, S[b][nt][p]);
-                                }
+                                    for (int nt = 0; nt < NT; ++nt) mma_p(acc[b][nt], a[p], S[b][nt][p]);
                             }
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
@@ -670,7 +687,7 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
             }
         }
         __syncthreads();                                // before the next row's queries and codes
-        if (u < units) rw = row_of(map, ub + u, Hkv, sets);
+        if (u < units) rw = row_of(map.at, ub + u, Hkv, sets);
     }
     if (stuck && lane == 0) atomicOr(status, (unsigned)FATHOM_DEV_TIMEOUT);
 }
@@ -679,7 +696,7 @@ store_attend_kernel(const __grid_constant__ AttendMap map, const void* __restric
 // none: the row's partials, in an order that depends on their number alone.
 constexpr int kMergeThreads = 256;
 __global__ void __launch_bounds__(kMergeThreads)
-store_attend_merge_kernel(const __grid_constant__ AttendMap map, const float* __restrict__ slots, int T, int Hq, int Hkv,
+store_attend_merge_kernel(const __grid_constant__ Spans<kAttendSets> map, const float* __restrict__ slots, int T, int Hq, int Hkv,
                           int sets, int pairs, int D, float* __restrict__ out, float* __restrict__ parts) {
     __shared__ float s_w[kMaxCtas];
     __shared__ float s_red[2][kMergeThreads / 32];
@@ -690,7 +707,7 @@ store_attend_merge_kernel(const __grid_constant__ AttendMap map, const float* __
     const int s = row / (Hkv * sets), rl = row % (Hkv * sets);
     const int g = rl / sets, pr = rl % sets * pairs + x;
     if (pr >= C) return;
-    const int ub = map.unit0[s] + rl * map.tiles[s], ue = ub + map.tiles[s];
+    const int ub = map.span[s].unit0 + rl * map.span[s].tiles, ue = ub + map.span[s].tiles;
     int p0 = 0, np = 0;
     if (ue > ub) {
         p0 = run_of(map, ub);
@@ -771,12 +788,12 @@ size_t store_attend_workspace_bytes(int S, int T, int Hq, int Hkv, int d) {
 namespace {
 
 struct Call {
-    AttendMap& map;
+    const AttendMap& map;
     const void* q;
     int q_dtype, T, Hq, Hkv, sets;
     float *slots, *out, *parts;
     cudaStream_t stream;
-    bool shared;   // some row's keys may be shared by several CTAs, or a row has none
+    Spans<kAttendSets> at;
     int P;
 };
 
@@ -809,40 +826,36 @@ bool tensor_maps(CUtensorMap* tm, CUtensorMap* stm, const uint32_t* planes, cons
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT, bool F32>
+template <int D, int NT, bool F32, int NS>
 cudaError_t launch_type(Call& a) {
     using Sh = Shape<D, NT, F32>;
     static_assert(Sh::kCtas * (Sh::kSmem + 1024) <= kMaxSmem + 1024, "the CTAs of an SM fit");
-    int64_t U = 0;
-    for (int s = 0; s < a.map.nsess; ++s) {
-        const int64_t last = a.map.visible[s] + a.T - 1;   // keys that the last token sees
-        const int64_t keys = last < a.map.n[s] ? (last > 0 ? last : 0) : a.map.n[s];
-        if (U > INT32_MAX / 16) return cudaErrorInvalidValue;   // unit and chunk numbers are 32 bits
-        a.map.unit0[s] = (int)U;
-        a.map.tiles[s] = (int)((keys + kTile - 1) / kTile);
-        U += (int64_t)a.map.tiles[s] * a.Hkv * a.sets;
-        a.shared = a.shared || a.map.tiles[s] != 1;
-    }
-    if (U > INT32_MAX / 16) return cudaErrorInvalidValue;
-    a.map.unit0[a.map.nsess] = (int)U;
-    if (U == 0) return cudaSuccess;
-    a.P = (int)(U < 148 * Sh::kCtas ? U : 148 * Sh::kCtas);
-    a.map.each = (int)(U / a.P);
-    a.map.more = (int)(U % a.P);
-    for (int s = 0; s < a.map.nsess; ++s)
-        if (!tensor_maps(&a.map.k_tm[s], &a.map.ks_tm[s], a.map.k_planes[s], a.map.k_scales[s], a.Hkv * D, D, a.map.k_pad[s]) ||
-            !tensor_maps(&a.map.v_tm[s], &a.map.vs_tm[s], a.map.v_planes[s], a.map.v_scales[s], a.Hkv * D, D, a.map.v_pad[s]))
+    const int U = a.at.each;   // all units
+    a.P = U < 148 * Sh::kCtas ? U : 148 * Sh::kCtas;
+    a.at.each = U / a.P;
+    a.at.more = U % a.P;
+    Sessions<NS> m;
+    m.at.nsess = a.at.nsess;
+    m.at.each = a.at.each;
+    m.at.more = a.at.more;
+    for (int s = 0; s < a.at.nsess; ++s) {
+        m.at.span[s] = a.at.span[s];
+        if (!tensor_maps(&m.k[s], &m.ks[s], a.map.k_planes[s], a.map.k_scales[s], a.Hkv * D, D, a.map.k_pad[s]) ||
+            !tensor_maps(&m.v[s], &m.vs[s], a.map.v_planes[s], a.map.v_scales[s], a.Hkv * D, D, a.map.v_pad[s]))
             return cudaErrorInvalidValue;
-    auto kern = store_attend_kernel<D, NT, F32>;
+    }
+    auto kern = store_attend_kernel<D, NT, F32, NS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, false, 1, a.map, a.q, a.q_dtype, a.T,
-                     a.Hq, a.Hkv, a.sets, a.slots, a.out, a.parts, device_status_ptr());
+    return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, false, 1, m, a.q, a.q_dtype, a.T, a.Hq, a.Hkv,
+                     a.sets, a.slots, a.out, a.parts, device_status_ptr());
 }
 
 template <int D, int NT>
 cudaError_t launch_tiles(Call& a) {
-    return a.q_dtype == FATHOM_F32 ? launch_type<D, NT, true>(a) : launch_type<D, NT, false>(a);
+    const bool f32 = a.q_dtype == FATHOM_F32;
+    if (a.at.nsess == 1) return f32 ? launch_type<D, NT, true, 1>(a) : launch_type<D, NT, false, 1>(a);
+    return f32 ? launch_type<D, NT, true, kAttendSets>(a) : launch_type<D, NT, false, kAttendSets>(a);
 }
 
 template <int D>
@@ -852,22 +865,40 @@ cudaError_t launch_dim(int nt, Call& a) {
 
 }  // namespace
 
-cudaError_t launch_store_attend(AttendMap& map, int Hkv, int d, const void* q, int q_dtype, int T, int Hq, float* out,
+cudaError_t launch_store_attend(const AttendMap& map, int Hkv, int d, const void* q, int q_dtype, int T, int Hq, float* out,
                                 float* parts, void* ws, cudaStream_t stream) {
     const int64_t C = (int64_t)T * (Hq / Hkv);
     const int nt = tiles_of_set(C), pairs = nt * kTilePairs;
-    Call a{map, q, q_dtype, T, Hq, Hkv, (int)((C + pairs - 1) / pairs), static_cast<float*>(ws), out, parts, stream, false, 0};
-    cudaError_t e;
-    switch (d) {
-        case 32: e = launch_dim<32>(nt, a); break;
-        case 64: e = launch_dim<64>(nt, a); break;
-        case 128: e = launch_dim<128>(nt, a); break;
-        case 256: e = launch_dim<256>(nt, a); break;
-        default: return cudaErrorInvalidValue;
+    Call a{map, q, q_dtype, T, Hq, Hkv, (int)((C + pairs - 1) / pairs), static_cast<float*>(ws), out, parts, stream, {}, 0};
+    a.at.nsess = map.nsess;
+    int64_t U = 0;
+    bool shared = false;   // some row's keys may be shared by several CTAs, or a row has none
+    for (int s = 0; s < map.nsess; ++s) {
+        const int64_t last = map.visible[s] + T - 1;   // keys that the last token sees
+        const int64_t keys = last < map.n[s] ? (last > 0 ? last : 0) : map.n[s];
+        Span& sp = a.at.span[s];
+        sp.n = (int)map.n[s];
+        sp.visible = (int)map.visible[s];
+        sp.unit0 = (int)U;
+        sp.tiles = (int)((keys + kTile - 1) / kTile);
+        U += (int64_t)sp.tiles * Hkv * a.sets;
+        if (U > INT32_MAX / 32) return cudaErrorInvalidValue;   // unit and chunk numbers are 32 bits
+        shared = shared || sp.tiles != 1;
     }
-    if (e != cudaSuccess || !a.shared) return e;
+    a.at.each = (int)U;
+    if (U > 0) {
+        cudaError_t e;
+        switch (d) {
+            case 32: e = launch_dim<32>(nt, a); break;
+            case 64: e = launch_dim<64>(nt, a); break;
+            case 128: e = launch_dim<128>(nt, a); break;
+            case 256: e = launch_dim<256>(nt, a); break;
+            default: return cudaErrorInvalidValue;
+        }
+        if (e != cudaSuccess || !shared) return e;
+    }
     return launch_ex(store_attend_merge_kernel, dim3((unsigned)((int64_t)map.nsess * Hkv * a.sets * pairs)),
-                     dim3(kMergeThreads), 0, stream, a.P > 0, 1, map, a.slots, T, Hq, Hkv, a.sets, pairs, d, out, parts);
+                     dim3(kMergeThreads), 0, stream, a.P > 0, 1, a.at, a.slots, T, Hq, Hkv, a.sets, pairs, d, out, parts);
 }
 
 }  // namespace fathom
