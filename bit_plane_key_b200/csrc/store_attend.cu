@@ -416,12 +416,12 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                         for (int p = 0; p < 4; ++p) S[b][nt][p][e] = 0.0f;
                     }
                 }
-#pragma unroll 1
-            for (int c = 0; c < 2 * NC; ++c, ++j) {
-                const bool isk = c < NC;
-                const int rj = j % kRing;
-                // ---- the chunk's planes of the warp's blocks to registers, as codes to the warp's own memory
-                stuck |= !barrier_wait(s_full + rj, (uint32_t)(j / kRing) & 1);
+            // chunk c of the tile, of K or of V: its planes of the warp's blocks to registers, as codes to the
+            // warp's own memory
+            auto stage = [&](bool isk, int c) {
+                const int rj = (2 * NC) % kRing == 0 ? c % kRing : j % kRing;
+                const uint32_t turn = (uint32_t)((2 * NC) % (2 * kRing) == 0 ? c / kRing : j / kRing) & 1;
+                stuck |= !barrier_wait(s_full + rj, turn);
                 uint2 W[2][4];                          // [channel of the pair][plane]
                 const uint2* src = reinterpret_cast<const uint2*>(s_raw + rj * Sh::kRaw) + pl * 16 + (wp ^ (pl & 7)) * 2 + blk;
 #pragma unroll
@@ -457,8 +457,8 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                         d4[r ^ ((pl >> 1) & 3)] = make_uint4(N[0][0][r], N[1][0][r], N[0][1][r], N[1][1][r]);
                 }
                 // warps take turns at the copy of the buffer's next chunk, once every warp has read this one
-                if (wp == j % kWarps && j + kRing < chunks) {
-                    stuck |= !barrier_wait(s_read + rj, (uint32_t)(j / kRing) & 1);
+                if (wp == ((2 * NC) % kWarps == 0 ? c : j) % kWarps && j + kRing < chunks) {
+                    stuck |= !barrier_wait(s_read + rj, turn);
                     const int cn = c + kRing, un = u + cn / (2 * NC);
                     if (lane == 0) {
                         if (un < re) copy(rw, ub + un, cn % (2 * NC), rj);
@@ -469,9 +469,13 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                     stuck |= !barrier_wait(s_read + kRing, u & 1);
                     if (lane == 0) copy_scale(u + 1 < re ? rw : row_of(map.at, ub + u + 1, Hkv, sets), ub + u + 1);
                 }
+                ++j;
                 __syncwarp();
-                if (!act) continue;
-                if (isk) {
+            };
+#pragma unroll 1
+            for (int c = 0; c < NC; ++c) {
+                stage(true, c);
+                if (act) {
                     // ---- S += codes . Q' of this chunk's channels
                     const uint32_t a15[4] = {0x000F000Fu, 0x000F000Fu, 0x000F000Fu, 0x000F000Fu};
                     const uint4* kc = reinterpret_cast<const uint4*>(codes);
@@ -516,8 +520,9 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                         }
                     }
                     __syncwarp();
-                    if (c < NC - 1) continue;
-
+                }
+            }
+            if (act) {
                     // ---- weights: lane (g, t) holds query t of the tile, 8 keys of each block
                     const bool cut = k0 + 2 * kBlock > least;   // some query of the set does not see all keys
                     float shift[NT];
@@ -606,12 +611,13 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                             neg[b][nt] = -0.5f * sum;
                             l[nt] = fmaf(sum, 512.0f / 15.0f, l[nt]);   // 2^24 / 2^15
                         }
-                } else {
-                    // ---- O += Delta (codes - 7.5) . P; the chunk's outputs are registers, so each chunk has its own code
-                    const uint4* vc = reinterpret_cast<const uint4*>(codes) + (lane ^ ((lane >> 3) & 3));
+            }
 #pragma unroll
-                    for (int cv = 0; cv < NC; ++cv)
-                        if (c == NC + cv) {
+            for (int cv = 0; cv < NC; ++cv) {
+                stage(false, NC + cv);
+                if (act) {
+                    // ---- O += Delta (codes - 7.5) . P
+                    const uint4* vc = reinterpret_cast<const uint4*>(codes) + (lane ^ ((lane >> 3) & 3));
 #pragma unroll
                         for (int k = 0; k < CK; ++k) {
                             const int mt = cv * CK + k;
@@ -636,7 +642,6 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                                     O[nt][mt][1] = fmaf(acc[b][nt][2] + acc[b][nt][3], dv.y, O[nt][mt][1]);
                                 }
                             }
-                        }
                         }
                     __syncwarp();
                 }
