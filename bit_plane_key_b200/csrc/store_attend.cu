@@ -283,12 +283,15 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         copy_scales(s_rs + Sh::kRawScales, &map.vs[r.s], b, r.g * D, s_full + kRing);
     };
     Row rw = row_of(map.at, ub, Hkv, sets);
+    // the merge may be scheduled as this grid's CTAs leave (they are all resident from the start)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == kThreads - 32) {                 // the first queries go to other warps
         for (int i = 0; i <= kRing; ++i) {
             barrier_init(s_full + i, 1);
             barrier_init(s_read + i, kWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        pdl_wait();
         copy_scale(rw, ub);
         for (int i = 0; i < kRing && i < chunks; ++i) {
             const int unit = ub + i / (2 * NC);
@@ -296,6 +299,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         }
     }
 
+    pdl_wait();
     bool stuck = false;
     uint32_t* codes = s_codes + wp * Sh::kOwn;
     uint16_t* scales = s_sc + wp * Sh::kScales;
@@ -706,27 +710,46 @@ store_attend_merge_kernel(const __grid_constant__ Spans<kAttendSets> map, const 
     __shared__ float s_w[kMaxCtas];
     __shared__ float s_red[2][kMergeThreads / 32];
     __shared__ float4 s_o[kMergeThreads];
-    pdl_wait();
+    constexpr int kFirst = 8;   // partials that a thread loads before it knows their weights
     const int G = Hq / Hkv, C = T * G;
     const int row = blockIdx.x / pairs, x = blockIdx.x % pairs;
     const int s = row / (Hkv * sets), rl = row % (Hkv * sets);
     const int g = rl / sets, pr = rl % sets * pairs + x;
-    if (pr >= C) return;
+    // (every CTA waits for the kernel before it, so that this one is not over sooner)
+    if (pr >= C) {
+        pdl_wait();
+        return;
+    }
     const int ub = map.span[s].unit0 + rl * map.span[s].tiles, ue = ub + map.span[s].tiles;
     int p0 = 0, np = 0;
     if (ue > ub) {
         p0 = run_of(map, ub);
         np = run_of(map, ue - 1) - p0 + 1;
-        if (np == 1) return;                     // written by its CTA
+        if (np == 1) {                           // written by its CTA
+            pdl_wait();
+            return;
+        }
     }
     const int64_t st = (int64_t)pairs * (D + 2);
     const float* base = slots + (int64_t)(p0 + row) * st;
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    float M = -INFINITY;
-    for (int p = threadIdx.x; p < np; p += kMergeThreads) {
-        const float v = base[p * st + pairs * D + x];
-        s_w[p] = v;
-        M = fmaxf(M, v);
+    // D/4 threads take a partial's channels, the others further partials
+    const int cl = D / 4, c4 = threadIdx.x % cl, grp = threadIdx.x / cl, ng = kMergeThreads / cl;
+    const float* mine = base + x * D + 4 * c4;
+    pdl_wait();
+    float4 v[kFirst];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int p = grp + i * ng;
+        v[i] = p < np ? *reinterpret_cast<const float4*>(mine + p * st) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    float M = -INFINITY, mp[(kMaxCtas + kMergeThreads - 1) / kMergeThreads], lp[(kMaxCtas + kMergeThreads - 1) / kMergeThreads];
+#pragma unroll
+    for (int i = 0; i < (kMaxCtas + kMergeThreads - 1) / kMergeThreads; ++i) {
+        const int p = threadIdx.x + i * kMergeThreads;
+        mp[i] = p < np ? base[p * st + pairs * D + x] : -INFINITY;
+        lp[i] = p < np ? base[p * st + pairs * (D + 1) + x] : 0.0f;
+        M = fmaxf(M, mp[i]);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -736,10 +759,14 @@ store_attend_merge_kernel(const __grid_constant__ Spans<kAttendSets> map, const 
     for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, s_red[0][w]);
     const float Mb = M == -INFINITY ? 0.0f : M;
     float L = 0.0f;
-    for (int p = threadIdx.x; p < np; p += kMergeThreads) {
-        const float f = ex2(s_w[p] - Mb);
-        s_w[p] = f;
-        L = fmaf(base[p * st + pairs * (D + 1) + x], f, L);
+#pragma unroll
+    for (int i = 0; i < (kMaxCtas + kMergeThreads - 1) / kMergeThreads; ++i) {
+        const int p = threadIdx.x + i * kMergeThreads;
+        if (p < np) {
+            const float f = ex2(mp[i] - Mb);
+            s_w[p] = f;
+            L = fmaf(lp[i], f, L);
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -748,23 +775,23 @@ store_attend_merge_kernel(const __grid_constant__ Spans<kAttendSets> map, const 
     L = 0.0f;
 #pragma unroll
     for (int w = 0; w < kMergeThreads / 32; ++w) L += s_red[1][w];
-    // D/4 threads take a partial's channels, the others further partials
-    const int cl = D / 4, c4 = threadIdx.x % cl, grp = threadIdx.x / cl, ng = kMergeThreads / cl;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int p = grp; p < np; p += ng) {
-        const float4 v = *reinterpret_cast<const float4*>(base + p * st + x * D + 4 * c4);
-        const float f = s_w[p];
-        o.x = fmaf(v.x, f, o.x);
-        o.y = fmaf(v.y, f, o.y);
-        o.z = fmaf(v.z, f, o.z);
-        o.w = fmaf(v.w, f, o.w);
-    }
+    auto take = [&](const float4& e, float f) {
+        o.x = fmaf(e.x, f, o.x);
+        o.y = fmaf(e.y, f, o.y);
+        o.z = fmaf(e.z, f, o.z);
+        o.w = fmaf(e.w, f, o.w);
+    };
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i)
+        if (grp + i * ng < np) take(v[i], s_w[grp + i * ng]);
+    for (int p = grp + kFirst * ng; p < np; p += ng) take(*reinterpret_cast<const float4*>(mine + p * st), s_w[p]);
     s_o[threadIdx.x] = o;
     __syncthreads();
     if (grp) return;
     for (int e = 1; e < ng; ++e) {
-        const float4 v = s_o[e * cl + c4];
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        const float4 w = s_o[e * cl + c4];
+        o.x += w.x, o.y += w.y, o.z += w.z, o.w += w.w;
     }
     const int64_t h = ((int64_t)s * T + pr / G) * Hq + g * G + pr % G;
     if (parts) {
@@ -852,7 +879,7 @@ cudaError_t launch_type(Call& a) {
     auto kern = store_attend_kernel<D, NT, F32, NS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, false, 1, m, a.q, a.q_dtype, a.T, a.Hq, a.Hkv,
+    return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, true, 1, m, a.q, a.q_dtype, a.T, a.Hq, a.Hkv,
                      a.sets, a.slots, a.out, a.parts, device_status_ptr());
 }
 
