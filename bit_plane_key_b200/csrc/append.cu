@@ -18,6 +18,8 @@
 // (x = X u, |X| <= 255, Delta = D v, D <= 2047, u and v powers of two: for
 // u >= v, x - m Delta is a multiple of v and 1/D of Delta or more; for u < v it
 // is a multiple of u, and Delta <= 2 |x| <= 510 u.)
+// The codes' clamp to [0, 15] is one of x, two channels at a time, to the bf16
+// nearest to +-8 Delta from inside: its quotient is in [-8, -7.9] or [7.9, 8).
 #include "fathom_internal.cuh"
 
 namespace fathom {
@@ -45,9 +47,63 @@ __device__ __forceinline__ void nibbles_to_planes(const uint32_t* N, uint32_t* W
     W[3] = (Q0 & 0x55555555u) | ((Q1 << 1) & 0xAAAAAAAAu);
 }
 
+// the bf16 next to +-8 Delta inside (-8 Delta may be reached, 8 Delta not), as bits
+__device__ __forceinline__ uint32_t low_bound(float delta) { return __float_as_uint(-8.0f * delta) >> 16; }
+__device__ __forceinline__ uint32_t high_bound(float delta) {
+    const uint32_t b = __float_as_uint(8.0f * delta);
+    return b == 0u ? 0u : (b - 1u) >> 16;   // the bits below 8 Delta, cut to bf16
+}
+
+// One block of a channel pair: x[i] = key i's two bf16 values, FULL: all 64 keys are there.
+template <bool FULL>
+__device__ __forceinline__ void pack_pair(const uint16_t* __restrict__ p, int64_t row_stride, int keys, uint32_t* __restrict__ s_w,
+                                          uint16_t* __restrict__ scale0, uint16_t* __restrict__ scale1) {
+    uint32_t x[kBlock];
+    __nv_bfloat162 mx = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kBlock; ++i) x[i] = FULL || i < keys ? *reinterpret_cast<const uint32_t*>(p + i * row_stride) : 0u;
+#pragma unroll
+    for (int i = 0; i < kBlock; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<__nv_bfloat162*>(&x[i])));
+    const __half d0 = __float2half_rn(__low2float(mx) * 0.125f), d1 = __float2half_rn(__high2float(mx) * 0.125f);
+    *scale0 = __half_as_ushort(d0);
+    *scale1 = __half_as_ushort(d1);
+    const float delta[2] = {__half2float(d0), __half2float(d1)};
+    const uint32_t lo = low_bound(delta[0]) | low_bound(delta[1]) << 16, hi = high_bound(delta[0]) | high_bound(delta[1]) << 16;
+#pragma unroll
+    for (int i = 0; i < kBlock; ++i) {
+        const __nv_bfloat162 v = __hmin2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), *reinterpret_cast<const __nv_bfloat162*>(&lo)),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&hi));
+        x[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const float inv = delta[e] > 0.0f ? __frcp_rn(delta[e]) : 0.0f;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint32_t N[4], W[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                // the floats 2^23 + code, shifted and added as they are, less their exponents
+                N[r] = 0u - 0x4B000000u * 0x11111111u;
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    const int i = 32 * w + 4 * m + r;
+                    const float v = __uint_as_float(e ? (x[i] & 0xFFFF0000u) : (x[i] << 16));
+                    const float u = __fmaf_rd(fmaf(fabsf(v), 4.76837158203125e-7f, v), inv, 8388616.0f);
+                    N[r] += (FULL || i < keys ? __float_as_uint(u) : 0x4B000000u) * (1u << (4 * m));
+                }
+            }
+            nibbles_to_planes(N, W);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s_w[e * 33 + j * 8 + w] = W[j];
+        }
+    }
+}
+
 __global__ void __launch_bounds__(2 * kMaxD)
 append_rows_kernel(AppendSide ks, AppendSide vs, int Hkv, int64_t rows_n, int64_t row_stride, int64_t blk0, int64_t n,
                    int d) {
+    pdl_wait();
     extern __shared__ uint32_t s_w[];   // [d][33]: channel's plane words [4][8], padded
     const int half = d / 2;
     const int b = threadIdx.x / half, cp = threadIdx.x - b * half;   // block of the group, channel pair
@@ -56,48 +112,14 @@ append_rows_kernel(AppendSide ks, AppendSide vs, int Hkv, int64_t rows_n, int64_
     const int64_t group = (blk0 / kGroup + blockIdx.x) * kGroup;     // first block of the group
     const int64_t blk = group + b;
     const int64_t rem = n - blk * kBlock;
-    const bool act = blk >= blk0 && rem > 0;
     const int64_t words = sd.n_pad / 32;
 
-    if (act) {
-        const int keys = rem < kBlock ? (int)rem : kBlock;
+    if (blk >= blk0 && rem > 0) {
         const uint16_t* p = sd.rows + ((int64_t)g * rows_n + blk * kBlock) * row_stride + 2 * cp;
-        uint32_t x[kBlock];
-        __nv_bfloat162 mx = __floats2bfloat162_rn(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < kBlock; ++i) {
-            x[i] = i < keys ? *reinterpret_cast<const uint32_t*>(p + i * row_stride) : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < kBlock; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<__nv_bfloat162*>(&x[i])));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float amax = e ? __high2float(mx) : __low2float(mx);
-            const __half dh = __float2half_rn(amax * 0.125f);
-            const float delta = __half2float(dh);
-            const float inv = delta > 0.0f ? __frcp_rn(delta) : 0.0f;
-            const int c = 2 * cp + e;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                uint32_t N[4], W[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    N[r] = 0u;
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        const int i = 32 * w + 4 * m + r;
-                        const float v = __uint_as_float(e ? (x[i] & 0xFFFF0000u) : (x[i] << 16));
-                        const float u = __fmaf_rd(fmaf(fabsf(v), 4.76837158203125e-7f, v), inv, 8388616.0f);
-                        const uint32_t code = __float_as_uint(fminf(fmaxf(u, 8388608.0f), 8388623.0f));
-                        N[r] += (i < keys ? code & 15u : 0u) << (4 * m);
-                    }
-                }
-                nibbles_to_planes(N, W);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s_w[c * 33 + j * 8 + 2 * b + w] = W[j];
-            }
-            sd.scales[((int64_t)g * d + c) * (sd.n_pad / kBlock) + blk] = __half_as_ushort(dh);
-        }
+        uint16_t* sc = sd.scales + ((int64_t)g * d + 2 * cp) * (sd.n_pad / kBlock) + blk;
+        uint32_t* w = s_w + 2 * cp * 33 + 2 * b;
+        if (rem >= kBlock) pack_pair<true>(p, row_stride, kBlock, w, sc, sc + sd.n_pad / kBlock);
+        else pack_pair<false>(p, row_stride, (int)rem, w, sc, sc + sd.n_pad / kBlock);
     }
     __syncthreads();
     // the group's words of every plane row: a whole sector, or the blocks that were packed
@@ -125,8 +147,8 @@ cudaError_t launch_append_rows(const uint16_t* K_rows, uint32_t* k_planes, uint1
     const AppendSide ks{K_rows, k_planes, k_scales, k_pad}, vs{V_rows, v_planes, v_scales, v_pad};
     const int64_t groups = ((n + kBlock - 1) / kBlock + kGroup - 1) / kGroup - blk0 / kGroup;
     dim3 grid((unsigned)groups, (unsigned)(V_rows ? 2 * Hkv : Hkv));
-    append_rows_kernel<<<grid, 2 * d, sizeof(uint32_t) * 33 * d, stream>>>(ks, vs, Hkv, rows_n, row_stride, blk0, n, d);
-    return cudaGetLastError();
+    return launch_ex(append_rows_kernel, grid, dim3(2 * d), sizeof(uint32_t) * 33 * d, stream, true, 1, ks, vs, Hkv,
+                     rows_n, row_stride, blk0, n, d);
 }
 
 }  // namespace fathom

@@ -95,13 +95,17 @@ def _check(rc, what):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    """The stream's handle (an int, which ctypes passes as a pointer); the current device's current stream by default."""
+    if stream is not None:
+        return stream.cuda_stream
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    # torch.cuda.current_stream() builds a Stream object for 3 us; this is the handle alone
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _dtype_code(t):
@@ -273,10 +277,7 @@ def scan_topk(store, q, depths, k, idx=None, top_scores=None, workspace=None, st
 
 
 def _store_array(stores):
-    arr = (fathom_store * len(stores))()
-    for i, st in enumerate(stores):
-        arr[i] = st._c
-    return arr
+    return (fathom_store * len(stores))(*[st._c for st in stores])
 
 
 def scan_batched_workspace_bytes(stores, n_q_heads, k):
@@ -421,20 +422,24 @@ def decode_step(store, q, sigma2, budget_bits, k, K_rows, V_rows, fixed_r=0, kv_
     return depths, idx, top_scores, out
 
 
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+
+
 def _check_rows(K_rows, V_rows):
     """Strides of a row cache, K_rows and V_rows [Hkv][rows][d]; returns (row stride, rows, host-resident)."""
-    rows_n = K_rows.shape[1]
-    if K_rows.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or V_rows.dtype != K_rows.dtype:
+    Hkv, rows_n, _ = shape = K_rows.shape
+    strides = K_rows.stride()
+    if K_rows.dtype not in _BF16_BITS or V_rows.dtype is not K_rows.dtype:
         raise TypeError("K_rows and V_rows hold bfloat16")
-    if (K_rows.shape != V_rows.shape or K_rows.stride() != V_rows.stride() or K_rows.stride(2) != 1
-            or (K_rows.shape[0] > 1 and K_rows.stride(0) != rows_n * K_rows.stride(1))
-            or K_rows.is_cuda != V_rows.is_cuda):
+    cuda = K_rows.is_cuda
+    if (shape != V_rows.shape or strides != V_rows.stride() or strides[2] != 1
+            or (Hkv > 1 and strides[0] != rows_n * strides[1]) or cuda != V_rows.is_cuda):
         raise ValueError("K_rows and V_rows need strides (rows*s, s, 1), the same for both")
-    return int(K_rows.stride(1)), int(rows_n), int(not K_rows.is_cuda)
+    return strides[1], rows_n, int(not cuda)
 
 
-def _check_out(t, shape, dtype, what):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+def _check_is(t, shape, dtype, what):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous %s %s" % (what, dtype, tuple(shape)))
 
 
@@ -446,33 +451,40 @@ def qk_norm_rope(qkv, n_q_heads, n_kv_heads, inv_freq, K_rows, V_rows, row0, q_w
     writes token t's key and value rows at row0 + t of the row cache (bf16 views
     as sparse_attend).  positions i32 [T], default row0 + t."""
     T, H, d = qkv.shape
-    if H != n_q_heads + 2 * n_kv_heads or qkv.stride(2) != 1 or (H > 1 and qkv.stride(1) != d):
+    ts, hs, cs = qkv.stride()
+    if H != n_q_heads + 2 * n_kv_heads or cs != 1 or (H > 1 and hs != d):
         raise ValueError("qkv must be [T][Hq + 2 Hkv][d] with a token's heads contiguous")
     stride, rows_n, host = _check_rows(K_rows, V_rows)
     if K_rows.shape[0] != n_kv_heads or K_rows.shape[2] != d:
         raise ValueError("K_rows and V_rows must be [Hkv][rows][d]")
     rot = 0
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _check_out(inv_freq, (rot // 2,), torch.float32, "inv_freq")
+        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous float32 [rot_dim / 2]")
+        rot = 2 * inv_freq.shape[0]
+    w_dtype = F32
+    if k_weight is not None and q_weight is None:
+        raise ValueError("q_weight and k_weight go together")
     for w in (q_weight, k_weight):
-        if w is not None and (w.numel() != d or not w.is_contiguous() or w.dtype != q_weight.dtype):
-            raise ValueError("q_weight and k_weight must be contiguous [d] of one dtype")
+        if w is not None:
+            if w.shape != (d,) or not w.is_contiguous() or w.dtype is not q_weight.dtype:
+                raise ValueError("q_weight and k_weight must be contiguous [d] of one dtype")
+            w_dtype = _dtype_code(w)
     if positions is not None:
-        _check_out(positions, (T,), torch.int32, "positions")
+        _check_is(positions, (T,), torch.int32, "positions")
     if out is None:
-        out = torch.empty((T, n_q_heads, d), dtype=qkv.dtype, device=qkv.device)
-    _check_out(out, (T, n_q_heads, d), qkv.dtype, "out")
+        out = qkv.new_empty((T, n_q_heads, d))
+    else:
+        _check_is(out, (T, n_q_heads, d), qkv.dtype, "out")
     if T == 0:
         return out
     # a single token has no stride of its own
-    ts = int(qkv.stride(0)) if T > 1 else H * d
-    _check(_lib.fathom_qk_norm_rope(_ptr(qkv), _dtype_code(qkv), ts, T, int(n_q_heads), int(n_kv_heads), d,
-                                    _ptr(q_weight), _ptr(k_weight),
-                                    _dtype_code(q_weight) if q_weight is not None else F32, float(eps),
-                                    _ptr(positions), _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(out),
-                                    _ptr(K_rows), _ptr(V_rows), stride, host, rows_n, int(row0), _stream(stream)),
-           "fathom_qk_norm_rope")
+    rc = _lib.fathom_qk_norm_rope(qkv.data_ptr(), _dtype_code(qkv), ts if T > 1 else H * d, T, int(n_q_heads), int(n_kv_heads), d,
+                                  _ptr(q_weight), _ptr(k_weight), w_dtype, float(eps), _ptr(positions), _ptr(inv_freq), rot,
+                                  bool(interleaved), out.data_ptr(), K_rows.data_ptr(), V_rows.data_ptr(), stride, host,
+                                  rows_n, int(row0), _stream(stream))
+    if rc:
+        _check(rc, "fathom_qk_norm_rope")
     return out
 
 
@@ -500,18 +512,25 @@ def store_attend_workspace_bytes(store, n_sessions, n_tokens, n_q_heads):
 
 def _attend_args(store, q, lead, out, width, workspace):
     """Checks q [lead...][Hq][d] and makes out f32 [lead...][Hq][width] and the workspace."""
-    if q.dim() != lead + 2 or q.shape[-1] != store.d or not q.is_contiguous():
-        raise ValueError("q must be contiguous with %d dimensions, the last of size %d" % (lead + 2, store.d))
-    shape = tuple(q.shape[:-1]) + (width,)
+    shape = q.shape
+    if len(shape) != lead + 2 or lead < 0 or shape[-1] != store.d or not q.is_contiguous():
+        raise ValueError("q must be contiguous [...][Hq][d] with d = %d" % store.d)
+    want = shape if width == store.d else shape[:-1] + (width,)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
-    _check_out(out, shape, torch.float32, "out")
-    S = q.shape[0] if lead == 2 else 1
-    T = q.shape[lead - 1] if lead else 1
+        out = q.new_empty(want, dtype=torch.float32)
+    else:
+        _check_is(out, want, torch.float32, "out")
+    T = shape[-3] if lead else 1
     if workspace is None:
-        nb = store_attend_workspace_bytes(store, S, T, q.shape[-2])
-        workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=q.device)
+        nb = store_attend_workspace_bytes(store, shape[0] if lead == 2 else 1, T, shape[-2])
+        workspace = q.new_empty(max(nb, 1), dtype=torch.uint8)
     return out, T, workspace
+
+
+def _attend_lead(q):
+    if q.dim() not in (2, 3):
+        raise ValueError("q must be [Hq][d] or [T][Hq][d]")
+    return q.dim() - 2
 
 
 def store_attend(k_store, v_store, q, causal=True, out=None, workspace=None, stream=None):
@@ -519,7 +538,7 @@ def store_attend(k_store, v_store, q, causal=True, out=None, workspace=None, str
     store: q [Hq][d] or [T][Hq][d] -> f32 of the same shape.  causal: the stores'
     last T keys are the T tokens' own, each sees its past and itself; else every
     token sees all keys."""
-    out, T, workspace = _attend_args(k_store, q, q.dim() - 2, out, k_store.d, workspace)
+    out, T, workspace = _attend_args(k_store, q, _attend_lead(q), out, k_store.d, workspace)
     _check(_lib.fathom_store_attend(k_store.c, v_store.c, _ptr(q), _dtype_code(q), T, q.shape[-2], int(bool(causal)),
                                     _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
            "fathom_store_attend")
@@ -529,7 +548,7 @@ def store_attend(k_store, v_store, q, causal=True, out=None, workspace=None, str
 def store_attend_partial(k_store, v_store, q, visible, parts=None, workspace=None, stream=None):
     """Partials f32 [..][Hq][d + 2] (as sparse_attend_partial) of attention over
     this range's keys; token t sees those below visible + t."""
-    parts, T, workspace = _attend_args(k_store, q, q.dim() - 2, parts, k_store.d + 2, workspace)
+    parts, T, workspace = _attend_args(k_store, q, _attend_lead(q), parts, k_store.d + 2, workspace)
     _check(_lib.fathom_store_attend_partial(k_store.c, v_store.c, _ptr(q), _dtype_code(q), T, q.shape[-2],
                                             int(visible), _ptr(parts), _ptr(workspace), workspace.numel(),
                                             _stream(stream)), "fathom_store_attend_partial")
