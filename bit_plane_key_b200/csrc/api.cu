@@ -512,15 +512,34 @@ int fathom_qk_norm_rope(const void* qkv, int dtype, int64_t token_stride, int n_
 }
 
 namespace {
-// A store that may be empty (n = 0) or about to grow to n_new keys.
-int resolve_growing(const fathom_store* s, int64_t n_new, const uint32_t** planes, const uint16_t** scales) {
-    if (!s || s->n < 0 || n_new < 1) return FATHOM_EINVAL;
-    fathom_store t = *s;
-    t.n = n_new;
-    const int rc = resolve_store(&t, planes, scales);
-    if (rc) return rc;
-    if (!s->host_resident && (!is_here(s->planes) || !is_here(s->scales))) return FATHOM_EINVAL;
+// A store that may be empty (n = 0) or about to grow to n_new keys: resolve_store's checks, its device
+// arrays on device `dev` (each pointer is looked up once: a batch has many).
+int resolve_growing(const fathom_store* s, int64_t n_new, int dev, const uint32_t** planes, const uint16_t** scales) {
+    if (!s || !s->planes || !s->scales || s->n < 0 || n_new < 1 || !dims_ok(s->n_kv_heads, s->d) ||
+        s->n_pad < n_pad_of(n_new) || s->n_pad % kPad || !aligned16(s->planes) || !aligned16(s->scales))
+        return FATHOM_EINVAL;
+    const void* at[2] = {s->planes, s->scales};
+    for (const void*& p : at) {
+        cudaPointerAttributes a;
+        if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+            cudaGetLastError();
+            return FATHOM_EINVAL;
+        }
+        if (s->host_resident) {
+            if (a.type != cudaMemoryTypeHost || !a.devicePointer) return FATHOM_EINVAL;
+            p = a.devicePointer;
+        } else if (a.type != cudaMemoryTypeManaged && (a.type != cudaMemoryTypeDevice || a.device != dev)) {
+            return FATHOM_EINVAL;
+        }
+    }
+    *planes = static_cast<const uint32_t*>(at[0]);
+    *scales = static_cast<const uint16_t*>(at[1]);
     return FATHOM_OK;
+}
+int current_device() {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    return dev;
 }
 }  // namespace
 
@@ -529,7 +548,8 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
                        fathom_stream_t stream) {
     const uint32_t *kp, *vp = nullptr;
     const uint16_t *ksc, *vsc = nullptr, *kr, *vr = nullptr;
-    int rc = resolve_growing(K, n_new, &kp, &ksc);
+    const int dev = current_device();
+    int rc = resolve_growing(K, n_new, dev, &kp, &ksc);
     if (rc) return rc;
     if (n_new <= K->n || rows_n < n_new || K == V || !V != !V_rows) return FATHOM_EINVAL;
     rc = resolve_rows(K_rows, row_stride, K->d, rows_host_resident, &kr);
@@ -537,11 +557,11 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
     if (V) {
         if (V->n != K->n || V->n_kv_heads != K->n_kv_heads || V->d != K->d || V->planes == K->planes)
             return FATHOM_EINVAL;
-        rc = resolve_growing(V, n_new, &vp, &vsc);
+        rc = resolve_growing(V, n_new, dev, &vp, &vsc);
         if (!rc) rc = resolve_rows(V_rows, row_stride, K->d, rows_host_resident, &vr);
         if (rc) return rc;
     }
-    if (K->n_kv_heads > 32767) return FATHOM_EUNSUPPORTED;   // heads of both stores along the grid's y
+    if (K->n_kv_heads > 65535) return FATHOM_EUNSUPPORTED;   // heads along the grid's y
     cudaError_t e = launch_append_rows(kr, const_cast<uint32_t*>(kp), const_cast<uint16_t*>(ksc), K->n_pad, vr,
                                        const_cast<uint32_t*>(vp), const_cast<uint16_t*>(vsc), V ? V->n_pad : 0,
                                        K->n_kv_heads, K->d, rows_n, row_stride, K->n / kBlock, n_new,
@@ -576,6 +596,7 @@ int store_attend(const fathom_store* Ks, const fathom_store* Vs, int S, const vo
     // sessions go in groups of kAttendSets, one launch each
     constexpr int kGroups = (kMaxSets + kAttendSets - 1) / kAttendSets;
     AttendMap maps[kGroups];
+    const int dev = current_device();
     for (int s = 0; s < S; ++s) {
         AttendMap& m = maps[s / kAttendSets];
         const int e = s % kAttendSets;
@@ -583,8 +604,8 @@ int store_attend(const fathom_store* Ks, const fathom_store* Vs, int S, const vo
         if (k.n_kv_heads != Hkv || v.n_kv_heads != Hkv || k.d != d || v.d != d || k.n != v.n || k.n > INT32_MAX)
             return FATHOM_EINVAL;
         // an empty store needs no arrays' contents, but is checked like any other
-        int rc = resolve_growing(&k, k.n > 0 ? k.n : 1, &m.k_planes[e], &m.k_scales[e]);
-        if (!rc) rc = resolve_growing(&v, v.n > 0 ? v.n : 1, &m.v_planes[e], &m.v_scales[e]);
+        int rc = resolve_growing(&k, k.n > 0 ? k.n : 1, dev, &m.k_planes[e], &m.k_scales[e]);
+        if (!rc) rc = resolve_growing(&v, v.n > 0 ? v.n : 1, dev, &m.v_planes[e], &m.v_scales[e]);
         if (rc) return rc;
         m.k_pad[e] = k.n_pad;
         m.v_pad[e] = v.n_pad;

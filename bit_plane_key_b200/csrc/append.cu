@@ -3,10 +3,14 @@
 // bit planes where they lie, both stores in one launch.  Codes, scales and
 // planes as pack_kernel writes them, bit for bit.
 //
-// One CTA per (four aligned 64-token blocks, KV head, store): four blocks
-// are 32 bytes of every plane row, one memory sector, so the planes leave as
-// whole sectors.  A thread holds two channels x 64 keys of one block in
-// registers (a warp's load reads 128 contiguous bytes of a row), so the
+// One CTA per (16 aligned 64-token blocks, 64 or 32 channels of a KV head,
+// store): 16 blocks are 128 bytes of every plane row, one line, and leave as one
+// write; a warp's load reads 128 (or 64) contiguous bytes of a row.  What bounds the
+// kernel is the number of pieces that memory moves: with 4 blocks to a CTA, its
+// planes written in pieces of 32 bytes, 131072 keys of 8 heads (d = 128), K and V,
+// took 155 us where this takes 130 (5.2 TB/s
+// of the 6.6 that a copy reaches).
+// A thread holds two channels x 64 keys of one block in registers, so the
 // block's largest magnitude needs no exchange.
 //
 // floor(x / Delta) without a division: with c = 2^23 + 8 and i = 1/Delta
@@ -25,7 +29,8 @@
 namespace fathom {
 namespace {
 
-constexpr int kGroup = 4;   // blocks per CTA: 256 keys, a 32-byte sector of a plane row
+constexpr int kGroup = 16;   // blocks per CTA: 1024 keys, a 128-byte line of a plane row
+constexpr int kSmall = 4;    // the same of few keys
 
 struct AppendSide {
     const uint16_t* rows;   // row of key i of head g at (g * rows_n + i) * row_stride
@@ -56,8 +61,8 @@ __device__ __forceinline__ uint32_t high_bound(float delta) {
 
 // One block of a channel pair: x[i] = key i's two bf16 values, FULL: all 64 keys are there.
 template <bool FULL>
-__device__ __forceinline__ void pack_pair(const uint16_t* __restrict__ p, int64_t row_stride, int keys, uint32_t* __restrict__ s_w,
-                                          uint16_t* __restrict__ scale0, uint16_t* __restrict__ scale1) {
+__device__ __forceinline__ void pack_pair(const uint16_t* __restrict__ p, int64_t row_stride, int keys, uint32_t* __restrict__ s_w, int plane_ld, int ld,
+                                          uint16_t* __restrict__ s_scale, int scale_ld) {
     uint32_t x[kBlock];
     __nv_bfloat162 mx = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
@@ -65,8 +70,8 @@ __device__ __forceinline__ void pack_pair(const uint16_t* __restrict__ p, int64_
 #pragma unroll
     for (int i = 0; i < kBlock; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<__nv_bfloat162*>(&x[i])));
     const __half d0 = __float2half_rn(__low2float(mx) * 0.125f), d1 = __float2half_rn(__high2float(mx) * 0.125f);
-    *scale0 = __half_as_ushort(d0);
-    *scale1 = __half_as_ushort(d1);
+    s_scale[0] = __half_as_ushort(d0);
+    s_scale[scale_ld] = __half_as_ushort(d1);
     const float delta[2] = {__half2float(d0), __half2float(d1)};
     const uint32_t lo = low_bound(delta[0]) | low_bound(delta[1]) << 16, hi = high_bound(delta[0]) | high_bound(delta[1]) << 16;
 #pragma unroll
@@ -95,46 +100,49 @@ __device__ __forceinline__ void pack_pair(const uint16_t* __restrict__ p, int64_
             }
             nibbles_to_planes(N, W);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s_w[e * 33 + j * 8 + w] = W[j];
+            for (int j = 0; j < 4; ++j) s_w[j * plane_ld + w * ld + e] = W[j];
         }
     }
 }
 
-__global__ void __launch_bounds__(2 * kMaxD)
-append_rows_kernel(AppendSide ks, AppendSide vs, int Hkv, int64_t rows_n, int64_t row_stride, int64_t blk0, int64_t n,
-                   int d) {
+// PAIRS channel pairs and GROUP blocks to a CTA
+template <int PAIRS, int GROUP>
+constexpr int threads_of() { return PAIRS * (GROUP < 8 ? GROUP : 256 / PAIRS); }
+template <int PAIRS, int GROUP>
+__global__ void __launch_bounds__((threads_of<PAIRS, GROUP>()), 512 / threads_of<PAIRS, GROUP>())
+append_rows_kernel(AppendSide ks, AppendSide vs, int64_t rows_n, int64_t row_stride, int64_t blk0, int64_t n, int d) {
+    constexpr int kThreads = threads_of<PAIRS, GROUP>(), kBlocks = kThreads / PAIRS;   // blocks at a time
+    constexpr int kLd = 2 * PAIRS + 1, kScaleLd = GROUP + 2, kWords = 2 * GROUP;
+    __shared__ uint32_t s_w[4 * kWords * kLd];             // [plane][word of the group][channel]
+    __shared__ uint16_t s_sc[2 * PAIRS * kScaleLd];        // [channel][block]
     pdl_wait();
-    extern __shared__ uint32_t s_w[];   // [d][33]: channel's plane words [4][8], padded
-    const int half = d / 2;
-    const int b = threadIdx.x / half, cp = threadIdx.x - b * half;   // block of the group, channel pair
-    const int g = blockIdx.y % Hkv;
-    const AppendSide& sd = blockIdx.y < Hkv ? ks : vs;
-    const int64_t group = (blk0 / kGroup + blockIdx.x) * kGroup;     // first block of the group
-    const int64_t blk = group + b;
-    const int64_t rem = n - blk * kBlock;
-    const int64_t words = sd.n_pad / 32;
-
-    if (blk >= blk0 && rem > 0) {
-        const uint16_t* p = sd.rows + ((int64_t)g * rows_n + blk * kBlock) * row_stride + 2 * cp;
-        uint16_t* sc = sd.scales + ((int64_t)g * d + 2 * cp) * (sd.n_pad / kBlock) + blk;
-        uint32_t* w = s_w + 2 * cp * 33 + 2 * b;
-        if (rem >= kBlock) pack_pair<true>(p, row_stride, kBlock, w, sc, sc + sd.n_pad / kBlock);
-        else pack_pair<false>(p, row_stride, (int)rem, w, sc, sc + sd.n_pad / kBlock);
+    const int tiles = d / (2 * PAIRS), c0 = blockIdx.z % tiles * 2 * PAIRS;
+    const AppendSide& sd = (int)blockIdx.z < tiles ? ks : vs;
+    const int64_t g = blockIdx.y, group = (blk0 / GROUP + blockIdx.x) * GROUP;   // head, first block of the group
+    const int64_t words = sd.n_pad / 32, blocks = sd.n_pad / kBlock;
+    const int cp = threadIdx.x % PAIRS;
+#pragma unroll 1
+    for (int b = threadIdx.x / PAIRS; b < GROUP; b += kBlocks) {
+        const int64_t blk = group + b, rem = n - blk * kBlock;
+        if (blk < blk0 || rem <= 0) continue;
+        const uint16_t* p = sd.rows + (g * rows_n + blk * kBlock) * row_stride + c0 + 2 * cp;
+        uint32_t* w = s_w + 2 * b * kLd + 2 * cp;
+        uint16_t* sc = s_sc + 2 * cp * kScaleLd + b;
+        if (rem >= kBlock) pack_pair<true>(p, row_stride, kBlock, w, kWords * kLd, kLd, sc, kScaleLd);
+        else pack_pair<false>(p, row_stride, (int)rem, w, kWords * kLd, kLd, sc, kScaleLd);
     }
     __syncthreads();
-    // the group's words of every plane row: a whole sector, or the blocks that were packed
-    const int64_t last = (n + kBlock - 1) / kBlock;
-    const int lo = blk0 > group ? (int)(blk0 - group) : 0;
-    const int hi = last - group < kGroup ? (int)(last - group) : kGroup;
-    for (int row = threadIdx.x; row < 4 * d; row += blockDim.x) {
-        const uint32_t* s = s_w + (row >> 2) * 33 + (row & 3) * 8;
-        uint32_t* o = sd.planes + ((int64_t)g * d * 4 + row) * words + group * 2;
-        if (lo == 0 && hi == kGroup) {
-            reinterpret_cast<uint4*>(o)[0] = make_uint4(s[0], s[1], s[2], s[3]);
-            reinterpret_cast<uint4*>(o)[1] = make_uint4(s[4], s[5], s[6], s[7]);
-        } else {
-            for (int e = lo; e < hi; ++e) reinterpret_cast<uint2*>(o)[e] = make_uint2(s[2 * e], s[2 * e + 1]);
-        }
+    // the plane rows' words and the scales of the blocks that were packed
+    const int wl = threadIdx.x % kWords;
+    if (group + wl / 2 >= blk0 && (group + wl / 2) * kBlock < n) {
+        uint32_t* o = sd.planes + (g * d + c0) * 4 * words + group * 2 + wl;
+        for (int row = threadIdx.x / kWords; row < 8 * PAIRS; row += kThreads / kWords)
+            o[row * words] = s_w[((row & 3) * kWords + wl) * kLd + (row >> 2)];
+    }
+    const int bl = threadIdx.x % GROUP;
+    if (group + bl >= blk0 && (group + bl) * kBlock < n) {
+        uint16_t* o = sd.scales + (g * d + c0) * blocks + group + bl;
+        for (int c = threadIdx.x / GROUP; c < 2 * PAIRS; c += kThreads / GROUP) o[c * blocks] = s_sc[c * kScaleLd + bl];
     }
 }
 
@@ -145,10 +153,21 @@ cudaError_t launch_append_rows(const uint16_t* K_rows, uint32_t* k_planes, uint1
                                int d, int64_t rows_n, int64_t row_stride, int64_t blk0, int64_t n,
                                cudaStream_t stream) {
     const AppendSide ks{K_rows, k_planes, k_scales, k_pad}, vs{V_rows, v_planes, v_scales, v_pad};
-    const int64_t groups = ((n + kBlock - 1) / kBlock + kGroup - 1) / kGroup - blk0 / kGroup;
-    dim3 grid((unsigned)groups, (unsigned)(V_rows ? 2 * Hkv : Hkv));
-    return launch_ex(append_rows_kernel, grid, dim3(2 * d), sizeof(uint32_t) * 33 * d, stream, true, 1, ks, vs, Hkv,
-                     rows_n, row_stride, blk0, n, d);
+    const int pairs = d % 64 == 0 ? 32 : 16, z = (V_rows ? 2 : 1) * (d / (2 * pairs));
+    const int64_t last = (n + kBlock - 1) / kBlock;   // blocks
+    auto groups = [&](int group) { return (last + group - 1) / group - blk0 / group; };
+    auto go = [&](auto kern, int group, int threads) {
+        return launch_ex(kern, dim3((unsigned)groups(group), (unsigned)Hkv, (unsigned)z), dim3(threads), 0, stream, true, 1,
+                         ks, vs, rows_n, row_stride, blk0, n, d);
+    };
+    // few keys: more CTAs of fewer blocks, rather than whole lines from CTAs that leave SMs idle
+    // (4097 keys, 2 heads of 64: 4.1 us against 6.6; 131072 keys, 8 heads of 128: 155 against 130)
+    if (groups(kGroup) * Hkv * z < 2 * 148) {
+        return pairs == 32 ? go(append_rows_kernel<32, kSmall>, kSmall, threads_of<32, kSmall>())
+                           : go(append_rows_kernel<16, kSmall>, kSmall, threads_of<16, kSmall>());
+    }
+    return pairs == 32 ? go(append_rows_kernel<32, kGroup>, kGroup, threads_of<32, kGroup>())
+                       : go(append_rows_kernel<16, kGroup>, kGroup, threads_of<16, kGroup>());
 }
 
 }  // namespace fathom
