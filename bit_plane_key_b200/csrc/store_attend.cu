@@ -255,7 +255,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
     // [ring][plane][channel][32 words], 16-byte pieces of a row swizzled by the channel's low 3 bits
     uint32_t* s_codes = s_raw + kRing * Sh::kRaw;       // [warp][block][ks][lane][4] code words
     uint16_t* s_rs = reinterpret_cast<uint16_t*>(s_codes + kWarps * Sh::kOwn);     // [K, V][D][blocks of the tile] scales, 16-byte pieces swizzled by the channel's bit 2
-    uint16_t* s_sc = s_rs + 2 * Sh::kRawScales;         // [warp][K, V][block][D] scales
+    uint16_t* s_sc = s_rs + 2 * Sh::kRawScales;         // [warp][K, V][block][D] scales, K's times the block's factor
     uint32_t* s_q = reinterpret_cast<uint32_t*>(s_sc + kWarps * Sh::kScales);      // [NT][ks][lane][4]
     uint32_t* s_q2 = s_q + Sh::kQWords;                 // [NT][ks][lane][2], f32 queries only
     float* s_m = reinterpret_cast<float*>(s_q2 + Sh::kQ2Words);   // [warp][pair]
@@ -285,17 +285,19 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
     Row rw = row_of(map.at, ub, Hkv, sets);
     // the merge may be scheduled as this grid's CTAs leave (they are all resident from the start)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == kThreads - 32) {                 // the first queries go to other warps
-        for (int i = 0; i <= kRing; ++i) {
-            barrier_init(s_full + i, 1);
-            barrier_init(s_read + i, kWarps);
+    if (wp == kWarps - 1) {                             // the first queries go to other warps
+        if (lane <= kRing) {
+            barrier_init(s_full + lane, 1);
+            barrier_init(s_read + lane, kWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
         pdl_wait();
-        copy_scale(rw, ub);
-        for (int i = 0; i < kRing && i < chunks; ++i) {
-            const int unit = ub + i / (2 * NC);
-            copy(unit < rw.u1 ? rw : row_of(map.at, unit, Hkv, sets), unit, i % (2 * NC), i);
+        if (lane == kRing) {
+            copy_scale(rw, ub);
+        } else if (lane < kRing && lane < chunks) {
+            const int unit = ub + lane / (2 * NC);
+            copy(unit < rw.u1 ? rw : row_of(map.at, unit, Hkv, sets), unit, lane % (2 * NC), lane);
         }
     }
 
@@ -370,7 +372,6 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
             const int k0 = (ub + u - rw.u0) * kTile + 2 * wp * kBlock;   // the warp's first block
             const bool act = k0 < most;
             // ---- the blocks' scales: 0 behind the last block that is seen, where memory may hold anything
-            __half2 sc2[2];
             float back[2];
             __syncwarp();
             {
@@ -383,11 +384,8 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 barrier_arrive(s_read + kRing);
 #pragma unroll
                 for (int i = 0; i < 2 * D / 32; ++i) {
-                    const uint32_t v = sw[i] & keep;
-                    if (i < D / 32) mh = __hmax2(mh, as_half2(v));
-                    uint16_t* dst = scales + (i < D / 32 ? 0 : 2 * D) + paired<CH>(32 * (i % (D / 32)) + lane);
-                    dst[0] = (uint16_t)v;
-                    dst[D] = (uint16_t)(v >> 16);
+                    sw[i] &= keep;
+                    if (i < D / 32) mh = __hmax2(mh, as_half2(sw[i]));
                 }
 #pragma unroll
                 for (int o = 16; o; o >>= 1) {
@@ -397,12 +395,22 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 // a power of two sc keeps Q' inside fp16: the block's largest scale times it is
                 // in [2^6, 2^7) (or sc is 2^15, the largest factor in fp16: Q' then has 22 bits
                 // below its largest still)
+                float sc[2];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const float dm = b ? __high2float(mh) : __low2float(mh);
                     const int ex = max((int)(__float_as_uint(dm) >> 23), 118);
-                    sc2[b] = __float2half2_rn(__uint_as_float((uint32_t)(260 - ex) << 23));
+                    sc[b] = __uint_as_float((uint32_t)(260 - ex) << 23);
                     back[b] = __uint_as_float((uint32_t)(ex + 18) << 23);   // 2^24 / sc
+                }
+                const __half2 sc2 = __floats2half2_rn(sc[0], sc[1]);
+#pragma unroll
+                for (int i = 0; i < 2 * D / 32; ++i) {
+                    __half2 v = as_half2(sw[i]);
+                    if (i < D / 32) v = __hmul2(v, sc2);
+                    __half* dst = reinterpret_cast<__half*>(scales) + (i < D / 32 ? 0 : 2 * D) + paired<CH>(32 * (i % (D / 32)) + lane);
+                    dst[0] = __low2half(v);
+                    dst[D] = __high2half(v);
                 }
             }
             // scores of 16-key tiles p; then, in [p][0] and [p][1], the bits of their weights as operands
@@ -491,8 +499,8 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const uint2 d4 = *reinterpret_cast<const uint2*>(scales + b * D + 16 * ks + 4 * lt);
-                            da[b] = __hmul2(as_half2(d4.x), sc2[b]);
-                            db[b] = __hmul2(as_half2(d4.y), sc2[b]);
+                            da[b] = as_half2(d4.x);
+                            db[b] = as_half2(d4.y);
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
