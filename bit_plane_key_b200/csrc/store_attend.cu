@@ -38,30 +38,34 @@ namespace {
 
 constexpr int kTilePairs = 4;                   // queries per 8 columns
 constexpr int kMaxCtas = 296;                   // two CTAs per SM
+
 constexpr int kWarps = 8;                       // of a CTA
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = kWarps * 2 * kBlock;      // keys: two blocks per warp, 128 bytes of every plane row
 
-template <int D, int NT, bool F32>
+// NB: blocks of a warp
+template <int D, int NT, bool F32, int NB>
 struct Shape {
-    static constexpr int kCtas = (NT == 1 && D <= 128) ? 2 : 1;   // per SM
+    static constexpr int kTileBlocks = kWarps * NB, kTile = kTileBlocks * kBlock;
+    static constexpr int kRow = kTileBlocks * 2;            // words of a plane row of the tile: 128 bytes, or 64
+    static constexpr int kCtas = (NT * NB <= 2 && D <= 128) ? 2 : 1;   // per SM
     static constexpr int kPairs = kTilePairs * NT;          // (token, head of the group) pairs of a set
     static constexpr int KS = D / 16;                       // 16-channel steps
     // a chunk: the tile's planes of CH channels of one operand; channels l and
     // l + HP of it are a pair
     static constexpr int CH = 32, CK = CH / 16, NC = D / CH, HP = CH / 2;
-    static constexpr int kRaw = CH * 4 * (kTile / 32);      // words of a chunk's planes
-    static constexpr int kRawScales = D * (kTile / kBlock); // halves of a tile's scales, of K or V
+    static constexpr int kRaw = CH * 4 * kRow;              // words of a chunk's planes
+    static constexpr int kRawScales = D * kTileBlocks;      // halves of a tile's scales, of K or V
     static constexpr int kRing = 4;
-    static constexpr int kCodes = 2 * CH * 8;               // words of a warp's codes of a chunk
+    static constexpr int kCodes = NB * CH * 8;              // words of a warp's codes of a chunk
     static constexpr int kOwn = kCodes > kPairs * D ? kCodes : kPairs * D;   // or of its partial outputs
-    static constexpr int kScales = 2 * 2 * D;               // halves: K, V; block; channels, pair by pair
+    static constexpr int kScales = 2 * NB * D;              // halves: K, V; block; channels, pair by pair
     static constexpr int kQWords = NT * KS * 32 * 4;        // a lane's share of the queries
     static constexpr int kQ2Words = F32 ? kQWords / 2 : 0;
     static constexpr size_t kBytes = 4 * (size_t)(kRing * kRaw + kWarps * kOwn) + 2 * (size_t)(kWarps * kScales + 2 * kRawScales) +
                                      4 * (size_t)(kQWords + kQ2Words) + 4 * (size_t)(2 * kWarps * kPairs + kPairs) +
                                      8 * 2 * (kRing + 1);
     static constexpr size_t kSmem = kBytes + 1024;          // the planes start on a 1024-byte boundary
+    static_assert(NB == 1 || NB == 2, "");
 };
 
 // where channel c of D lies when channels are listed pair by pair
@@ -243,18 +247,19 @@ __device__ __noinline__ Row row_of(const Spans<S>& m, int u, int Hkv, int sets) 
     return r;
 }
 
-template <int D, int NT, bool F32, int NS>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT, F32>::kCtas)
+template <int D, int NT, bool F32, int NS, int NB>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT, F32, NB>::kCtas))
 store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __restrict__ q, int q_dtype, int T, int Hq,
                     int Hkv, int sets, float* __restrict__ slots, float* __restrict__ out, float* __restrict__ parts,
                     unsigned int* status) {
-    using Sh = Shape<D, NT, F32>;
+    using Sh = Shape<D, NT, F32, NB>;
+    constexpr int kTile = Sh::kTile;
     constexpr int KS = Sh::KS, CH = Sh::CH, CK = Sh::CK, NC = Sh::NC, HP = Sh::HP, kPairs = Sh::kPairs, kRing = Sh::kRing;
     extern __shared__ uint32_t smem_raw[];
     uint32_t* s_raw = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u) / 4;   // the next 1024-byte boundary
-    // [ring][plane][channel][32 words], 16-byte pieces of a row swizzled by the channel's low 3 bits
+    // [ring][plane][channel][row of the tile], 16-byte pieces swizzled by the channel
     uint32_t* s_codes = s_raw + kRing * Sh::kRaw;       // [warp][block][ks][lane][4] code words
-    uint16_t* s_rs = reinterpret_cast<uint16_t*>(s_codes + kWarps * Sh::kOwn);     // [K, V][D][blocks of the tile] scales, 16-byte pieces swizzled by the channel's bit 2
+    uint16_t* s_rs = reinterpret_cast<uint16_t*>(s_codes + kWarps * Sh::kOwn);     // [K, V][D][blocks of the tile] scales, the 16-byte pieces of 32 swizzled by the channel's bit 2
     uint16_t* s_sc = s_rs + 2 * Sh::kRawScales;         // [warp][K, V][block][D] scales, K's times the block's factor
     uint32_t* s_q = reinterpret_cast<uint32_t*>(s_sc + kWarps * Sh::kScales);      // [NT][ks][lane][4]
     uint32_t* s_q2 = s_q + Sh::kQWords;                 // [NT][ks][lane][2], f32 queries only
@@ -369,18 +374,22 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         __syncthreads();                                // the queries are in place
 
         for (; u < re; ++u) {
-            const int k0 = (ub + u - rw.u0) * kTile + 2 * wp * kBlock;   // the warp's first block
+            const int k0 = (ub + u - rw.u0) * kTile + NB * wp * kBlock;   // the warp's first block
             const bool act = k0 < most;
             // ---- the blocks' scales: 0 behind the last block that is seen, where memory may hold anything
-            float back[2];
+            float back[NB];
             __syncwarp();
             {
-                const uint32_t keep = act ? (k0 + kBlock < most ? 0xFFFFFFFFu : 0xFFFFu) : 0u;
+                const uint32_t keep = act ? (NB == 2 && k0 + kBlock < most ? 0xFFFFFFFFu : 0xFFFFu) : 0u;
                 __half2 mh = __float2half2_rn(0.0f);
                 stuck |= !barrier_wait(s_full + kRing, u & 1);
-                uint32_t sw[2 * D / 32];                // of two blocks: K's channels, then V's
+                uint32_t sw[2 * D / 32];                // of the warp's blocks: K's channels, then V's
 #pragma unroll
-                for (int i = 0; i < 2 * D / 32; ++i) sw[i] = reinterpret_cast<const uint32_t*>(s_rs)[(32 * i + lane) * (kTile / kBlock / 2) + (wp ^ (lane & 4))];
+                for (int i = 0; i < 2 * D / 32; ++i) {
+                    const int word = (NB * wp / 2) ^ (NB == 2 ? lane & 4 : 0);
+                    sw[i] = reinterpret_cast<const uint32_t*>(s_rs)[(32 * i + lane) * (Sh::kTileBlocks / 2) + word];
+                    if (NB == 1 && (wp & 1)) sw[i] >>= 16;
+                }
                 barrier_arrive(s_read + kRing);
 #pragma unroll
                 for (int i = 0; i < 2 * D / 32; ++i) {
@@ -395,9 +404,9 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 // a power of two sc keeps Q' inside fp16: the block's largest scale times it is
                 // in [2^6, 2^7) (or sc is 2^15, the largest factor in fp16: Q' then has 22 bits
                 // below its largest still)
-                float sc[2];
+                float sc[2] = {1.0f, 1.0f};
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < NB; ++b) {
                     const float dm = b ? __high2float(mh) : __low2float(mh);
                     const int ex = max((int)(__float_as_uint(dm) >> 23), 118);
                     sc[b] = __uint_as_float((uint32_t)(260 - ex) << 23);
@@ -408,16 +417,17 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 for (int i = 0; i < 2 * D / 32; ++i) {
                     __half2 v = as_half2(sw[i]);
                     if (i < D / 32) v = __hmul2(v, sc2);
-                    __half* dst = reinterpret_cast<__half*>(scales) + (i < D / 32 ? 0 : 2 * D) + paired<CH>(32 * (i % (D / 32)) + lane);
+                    __half* dst = reinterpret_cast<__half*>(scales) + (i < D / 32 ? 0 : NB * D) + paired<CH>(32 * (i % (D / 32)) + lane);
                     dst[0] = __low2half(v);
-                    dst[D] = __high2half(v);
+                    if (NB == 2) dst[D] = __high2half(v);
                 }
             }
             // scores of 16-key tiles p; then, in [p][0] and [p][1], the bits of their weights as operands
-            float S[2][NT][4][4], B15[2][NT][4], neg[2][NT];
-            const int pl = (lane & 7) + 8 * (lane >> 4), blk = (lane >> 3) & 1;   // the lane's channel pair and block
+            float S[NB][NT][4][4], B15[NB][NT][4], neg[NB][NT];
+            // the lane's channel pair, and its block (of two) or word (of one block)
+            const int pl = NB == 2 ? (lane & 7) + 8 * (lane >> 4) : lane >> 1, part = NB == 2 ? (lane >> 3) & 1 : lane & 1;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     neg[b][nt] = 0.0f;
@@ -434,39 +444,66 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 const int rj = (2 * NC) % kRing == 0 ? c % kRing : j % kRing;
                 const uint32_t turn = (uint32_t)((2 * NC) % (2 * kRing) == 0 ? c / kRing : j / kRing) & 1;
                 stuck |= !barrier_wait(s_full + rj, turn);
-                uint2 W[2][4];                          // [channel of the pair][plane]
-                const uint2* src = reinterpret_cast<const uint2*>(s_raw + rj * Sh::kRaw) + pl * 16 + (wp ^ (pl & 7)) * 2 + blk;
+                // pieces of 16 bytes: a warp's two blocks of 128 keys, or the two warps' of 64 that share one
+                const uint32_t* src = s_raw + rj * Sh::kRaw + pl * Sh::kRow;
+                const int piece = NB == 2 ? wp : wp / 2, swizzle = NB == 2 ? pl & 7 : (pl >> 1) & 3;
+                src += (piece ^ swizzle) * 4 + (NB == 2 ? 2 * part : 2 * (wp & 1) + part);
+                // both code layouts keep the lanes of a write, and of a read, on different banks
+                if (NB == 2) {
+                    uint2 P[2][4];                      // [channel of the pair][plane]
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) W[e][k] = src[(k * CH + e * HP) * 16];
-                // the last warp to have read a buffer has the next chunk copied into it
-                barrier_arrive(s_read + rj);
-                uint32_t N[2][2][4];                    // [channel][word][r]
+                        for (int k = 0; k < 4; ++k) P[e][k] = *reinterpret_cast<const uint2*>(src + (k * CH + e * HP) * Sh::kRow);
+                    barrier_arrive(s_read + rj);
+                    uint32_t N[2][2][4];                // [channel][word][r]
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    planes_to_nibbles(W[e][0].x, W[e][1].x, W[e][2].x, W[e][3].x, N[e][0]);
-                    planes_to_nibbles(W[e][0].y, W[e][1].y, W[e][2].y, W[e][3].y, N[e][1]);
-                }
-                uint32_t* dst = codes + blk * (Sh::kCodes / 2) + (pl >> 3) * 128;
-                // both layouts keep the lanes of a write, and of a read, on different banks
-                if (isk) {
-                    // row g of the second block lies where row g ^ 1 would
-                    uint2* d2 = reinterpret_cast<uint2*>(dst) + (pl & 7);
+                    for (int e = 0; e < 2; ++e) {
+                        planes_to_nibbles(P[e][0].x, P[e][1].x, P[e][2].x, P[e][3].x, N[e][0]);
+                        planes_to_nibbles(P[e][0].y, P[e][1].y, P[e][2].y, P[e][3].y, N[e][1]);
+                    }
+                    uint32_t* dst = codes + part * (Sh::kCodes / 2) + (pl >> 3) * 128;
+                    if (isk) {
+                        // row g of the second block lies where row g ^ 1 would
+                        uint2* d2 = reinterpret_cast<uint2*>(dst) + (pl & 7);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
+                        for (int r = 0; r < 4; ++r)
 #pragma unroll
-                        for (int k4 = 0; k4 < 2; ++k4) {
-                            const uint32_t sel = k4 ? 0x7632u : 0x5410u;
-                            d2[(2 * r + (k4 ^ blk)) * 8] = make_uint2(__byte_perm(N[0][0][r], N[1][0][r], sel),
-                                                                      __byte_perm(N[0][1][r], N[1][1][r], sel));
-                        }
+                            for (int k4 = 0; k4 < 2; ++k4) {
+                                const uint32_t sel = k4 ? 0x7632u : 0x5410u;
+                                d2[(2 * r + (k4 ^ part)) * 8] = make_uint2(__byte_perm(N[0][0][r], N[1][0][r], sel),
+                                                                           __byte_perm(N[0][1][r], N[1][1][r], sel));
+                            }
+                    } else {
+                        // column pair t of row g lies where t ^ (g / 2) would
+                        uint4* d4 = reinterpret_cast<uint4*>(dst) + (pl & 7) * 4;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            d4[r ^ ((pl >> 1) & 3)] = make_uint4(N[0][0][r], N[1][0][r], N[0][1][r], N[1][1][r]);
+                    }
                 } else {
-                    // column pair t of row g lies where t ^ (g / 2) would
-                    uint4* d4 = reinterpret_cast<uint4*>(dst) + (pl & 7) * 4;
+                    uint32_t P[2][4], N[2][4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        d4[r ^ ((pl >> 1) & 3)] = make_uint4(N[0][0][r], N[1][0][r], N[0][1][r], N[1][1][r]);
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) P[e][k] = src[(k * CH + e * HP) * Sh::kRow];
+                    barrier_arrive(s_read + rj);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) planes_to_nibbles(P[e][0], P[e][1], P[e][2], P[e][3], N[e]);
+                    uint32_t* dst = codes + (pl >> 3) * 128;
+                    if (isk) {
+                        // row g of an odd 16-channel step lies where row g ^ 1 would
+                        dst += (pl & 7) * 2 + part;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int k4 = 0; k4 < 2; ++k4)
+                                dst[(2 * r + (k4 ^ (pl >> 3))) * 16] = __byte_perm(N[0][r], N[1][r], k4 ? 0x7632u : 0x5410u);
+                    } else {
+                        uint2* d2 = reinterpret_cast<uint2*>(dst) + (pl & 7) * 8 + part;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) d2[(r ^ ((pl >> 1) & 3)) * 2] = make_uint2(N[0][r], N[1][r]);
+                    }
                 }
                 // warps take turns at the copy of the buffer's next chunk, once every warp has read this one
                 if (wp == ((2 * NC) % kWarps == 0 ? c : j) % kWarps && j + kRing < chunks) {
@@ -494,10 +531,10 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
 #pragma unroll
                     for (int k = 0; k < CK; ++k) {
                         const int ks = c * CK + k;
-                        uint32_t bq[2][NT][2];
-                        __half2 da[2], db[2];
+                        uint32_t bq[NB][NT][2];
+                        __half2 da[NB], db[NB];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
+                        for (int b = 0; b < NB; ++b) {
                             const uint2 d4 = *reinterpret_cast<const uint2*>(scales + b * D + 16 * ks + 4 * lt);
                             da[b] = as_half2(d4.x);
                             db[b] = as_half2(d4.y);
@@ -508,7 +545,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                             uint2 q2 = make_uint2(0u, 0u);
                             if (F32) q2 = *reinterpret_cast<const uint2*>(s_q2 + ((nt * KS + ks) * 32 + lane) * 2);
 #pragma unroll
-                            for (int b = 0; b < 2; ++b) {
+                            for (int b = 0; b < NB; ++b) {
                                 // even column: z = rn(q1 d); odd: z = q1 d - rn(q1 d), exact, + q2 d
                                 __half2 za = __hfma2(as_half2(q4.z), da[b], __hmul2_rn(as_half2(q4.x), da[b]));
                                 __half2 zb = __hfma2(as_half2(q4.w), db[b], __hmul2_rn(as_half2(q4.y), db[b]));
@@ -522,9 +559,9 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                             }
                         }
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
+                        for (int b = 0; b < NB; ++b) {
                             uint32_t a[4][4];
-                            operands(kc[b * (Sh::kCodes / 8) + k * 32 + (lane ^ (b * 4))], a);
+                            operands(kc[b * (Sh::kCodes / (4 * NB)) + k * 32 + (lane ^ (NB == 2 ? b * 4 : (k & 1) * 4))], a);
 #pragma unroll
                             for (int p = 0; p < 4; ++p)
 #pragma unroll
@@ -536,16 +573,16 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
             }
             if (act) {
                     // ---- weights: lane (g, t) holds query t of the tile, 8 keys of each block
-                    const bool cut = k0 + 2 * kBlock > least;   // some query of the set does not see all keys
+                    const bool cut = k0 + NB * kBlock > least;   // some query of the set does not see all keys
                     float shift[NT];
                     bool moved = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float f = s_f[nt * kTilePairs + lt];
-                        float F[2];
+                        float F[NB];
                         float mn = m[nt];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
+                        for (int b = 0; b < NB; ++b) {
                             const float off = -0.5f * (B15[b][nt][0] + B15[b][nt][1]);
                             float mx = -INFINITY;
 #pragma unroll
@@ -571,7 +608,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                         // the exponents that matter, both are rounded alike instead
                         if (fabsf(base) > 1048576.0f) {
 #pragma unroll
-                            for (int b = 0; b < 2; ++b) {
+                            for (int b = 0; b < NB; ++b) {
 #pragma unroll
                                 for (int p = 0; p < 4; ++p) {
                                     S[b][nt][p][0] *= F[b];
@@ -584,7 +621,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                         moved |= mn != m[nt];
                         m[nt] = mn;
 #pragma unroll
-                        for (int b = 0; b < 2; ++b)
+                        for (int b = 0; b < NB; ++b)
 #pragma unroll
                             for (int p = 0; p < 4; ++p) {
                                 // weights times 2^15, or 2^11 where the codes come 16 times as large
@@ -612,7 +649,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
+                        for (int b = 0; b < NB; ++b) {
                             float c4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                             for (int p = 0; p < 4; ++p) {
@@ -633,11 +670,11 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
 #pragma unroll
                         for (int k = 0; k < CK; ++k) {
                             const int mt = cv * CK + k;
-                            float acc[2][NT][4];
+                            float acc[NB][NT][4];
 #pragma unroll
-                            for (int b = 0; b < 2; ++b) {
+                            for (int b = 0; b < NB; ++b) {
                                 uint32_t a[4][4];
-                                operands(vc[b * (Sh::kCodes / 8) + k * 32], a);
+                                operands(vc[b * (Sh::kCodes / (4 * NB)) + k * 32], a);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) acc[b][nt][0] = acc[b][nt][2] = neg[b][nt], acc[b][nt][1] = acc[b][nt][3] = 0.0f;
 #pragma unroll
@@ -646,8 +683,8 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                                     for (int nt = 0; nt < NT; ++nt) mma_p(acc[b][nt], a[p], S[b][nt][p]);
                             }
 #pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                const float2 dv = __half22float2(*reinterpret_cast<const __half2*>(scales + (2 + b) * D + 16 * mt + 2 * lg));
+                            for (int b = 0; b < NB; ++b) {
+                                const float2 dv = __half22float2(*reinterpret_cast<const __half2*>(scales + (NB + b) * D + 16 * mt + 2 * lg));
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
                                     O[nt][mt][0] = fmaf(acc[b][nt][0] + acc[b][nt][1], dv.x, O[nt][mt][0]);
@@ -835,6 +872,7 @@ struct Call {
     cudaStream_t stream;
     Spans<kAttendSets> at;
     int P;
+    bool shared;   // some row's keys may be shared by several CTAs, or a row has none
 };
 
 // The tensor maps of a store: planes as words, channels of all heads, planes, a box
@@ -842,7 +880,7 @@ struct Call {
 // of each row swizzled by the row number; scales as blocks, channels of all
 // heads, a box being a tile's blocks of a head's channels.
 bool tensor_maps(CUtensorMap* tm, CUtensorMap* stm, const uint32_t* planes, const uint16_t* scales, int channels, int d,
-                 int64_t n_pad) {
+                 int64_t n_pad, int tile) {
     using Encode = decltype(&cuTensorMapEncodeTiled);
     static const Encode encode = [] {
         void* f = nullptr;
@@ -855,22 +893,42 @@ bool tensor_maps(CUtensorMap* tm, CUtensorMap* stm, const uint32_t* planes, cons
     if (!encode) return false;
     const cuuint64_t row = (cuuint64_t)(n_pad / 8);
     const cuuint64_t dims[3] = {row / 4, (cuuint64_t)channels, 4}, strides[2] = {4 * row, row};
-    const cuuint32_t box[3] = {kTile / 32, 32, 4}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)tile / 32, 32, 4}, step[3] = {1, 1, 1};
     const cuuint64_t sdims[2] = {(cuuint64_t)(n_pad / kBlock), (cuuint64_t)channels}, sstrides[1] = {(cuuint64_t)(n_pad / kBlock) * 2};
-    const cuuint32_t sbox[2] = {kTile / kBlock, (cuuint32_t)d};
+    const cuuint32_t sbox[2] = {(cuuint32_t)tile / kBlock, (cuuint32_t)d};
     return encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint32_t*>(planes), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, tile == 1024 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
            encode(stm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint16_t*>(scales), sdims, sstrides, sbox, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, tile == 1024 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT, bool F32, int NS>
-cudaError_t launch_type(Call& a) {
-    using Sh = Shape<D, NT, F32>;
+// Lays the sessions out in tiles; the number of units, or -1 if unit and chunk numbers would not fit 32 bits.
+int lay_out(Call& a, int tile) {
+    int64_t U = 0;
+    for (int s = 0; s < a.map.nsess; ++s) {
+        const int64_t last = a.map.visible[s] + a.T - 1;   // keys that the last token sees
+        const int64_t keys = last < a.map.n[s] ? (last > 0 ? last : 0) : a.map.n[s];
+        Span& sp = a.at.span[s];
+        sp.n = (int)a.map.n[s];
+        sp.visible = (int)a.map.visible[s];
+        sp.unit0 = (int)U;
+        sp.tiles = (int)((keys + tile - 1) / tile);
+        U += (int64_t)sp.tiles * a.Hkv * a.sets;
+        if (U > INT32_MAX / 32) return -1;
+        a.shared = a.shared || sp.tiles != 1;
+    }
+    return (int)U;
+}
+
+template <int D, int NT, bool F32, int NS, int NB>
+cudaError_t launch_shape(Call& a) {
+    using Sh = Shape<D, NT, F32, NB>;
     static_assert(Sh::kCtas * (Sh::kSmem + 1024) <= kMaxSmem + 1024, "the CTAs of an SM fit");
-    const int U = a.at.each;   // all units
+    a.shared = false;
+    const int U = lay_out(a, Sh::kTile);
+    if (U < 0) return cudaErrorInvalidValue;
     a.P = U < 148 * Sh::kCtas ? U : 148 * Sh::kCtas;
     a.at.each = U / a.P;
     a.at.more = U % a.P;
@@ -880,27 +938,31 @@ cudaError_t launch_type(Call& a) {
     m.at.more = a.at.more;
     for (int s = 0; s < a.at.nsess; ++s) {
         m.at.span[s] = a.at.span[s];
-        if (!tensor_maps(&m.k[s], &m.ks[s], a.map.k_planes[s], a.map.k_scales[s], a.Hkv * D, D, a.map.k_pad[s]) ||
-            !tensor_maps(&m.v[s], &m.vs[s], a.map.v_planes[s], a.map.v_scales[s], a.Hkv * D, D, a.map.v_pad[s]))
+        if (!tensor_maps(&m.k[s], &m.ks[s], a.map.k_planes[s], a.map.k_scales[s], a.Hkv * D, D, a.map.k_pad[s], Sh::kTile) ||
+            !tensor_maps(&m.v[s], &m.vs[s], a.map.v_planes[s], a.map.v_scales[s], a.Hkv * D, D, a.map.v_pad[s], Sh::kTile))
             return cudaErrorInvalidValue;
     }
-    auto kern = store_attend_kernel<D, NT, F32, NS>;
+    auto kern = store_attend_kernel<D, NT, F32, NS, NB>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
     if (e != cudaSuccess) return e;
     return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, true, 1, m, a.q, a.q_dtype, a.T, a.Hq, a.Hkv,
                      a.sets, a.slots, a.out, a.parts, device_status_ptr());
 }
 
-template <int D, int NT>
-cudaError_t launch_tiles(Call& a) {
-    const bool f32 = a.q_dtype == FATHOM_F32;
-    if (a.at.nsess == 1) return f32 ? launch_type<D, NT, true, 1>(a) : launch_type<D, NT, false, 1>(a);
-    return f32 ? launch_type<D, NT, true, kAttendSets>(a) : launch_type<D, NT, false, kAttendSets>(a);
+template <int D, int NT, bool F32>
+cudaError_t launch_type(Call& a, int units) {
+    if (a.at.nsess > 1) return launch_shape<D, NT, F32, kAttendSets, 2>(a);
+    // few keys: half as long tiles, as long as all run at once (1 head of 128, 4096 keys: 9.0 us against
+    // 11.4; 2 heads of 256, 8 queries each, 70001 keys, whose half tiles would not: 36 us against 27)
+    if (2 * units <= 148 * Shape<D, NT, F32, 1>::kCtas) return launch_shape<D, NT, F32, 1, 1>(a);
+    return launch_shape<D, NT, F32, 1, 2>(a);
 }
 
 template <int D>
-cudaError_t launch_dim(int nt, Call& a) {
-    return nt == 1 ? launch_tiles<D, 1>(a) : launch_tiles<D, 2>(a);
+cudaError_t launch_dim(int nt, Call& a, int units) {
+    const bool f32 = a.q_dtype == FATHOM_F32;
+    if (nt == 1) return f32 ? launch_type<D, 1, true>(a, units) : launch_type<D, 1, false>(a, units);
+    return f32 ? launch_type<D, 2, true>(a, units) : launch_type<D, 2, false>(a, units);
 }
 
 }  // namespace
@@ -909,33 +971,20 @@ cudaError_t launch_store_attend(const AttendMap& map, int Hkv, int d, const void
                                 float* parts, void* ws, cudaStream_t stream) {
     const int64_t C = (int64_t)T * (Hq / Hkv);
     const int nt = tiles_of_set(C), pairs = nt * kTilePairs;
-    Call a{map, q, q_dtype, T, Hq, Hkv, (int)((C + pairs - 1) / pairs), static_cast<float*>(ws), out, parts, stream, {}, 0};
+    Call a{map, q, q_dtype, T, Hq, Hkv, (int)((C + pairs - 1) / pairs), static_cast<float*>(ws), out, parts, stream, {}, 0, false};
     a.at.nsess = map.nsess;
-    int64_t U = 0;
-    bool shared = false;   // some row's keys may be shared by several CTAs, or a row has none
-    for (int s = 0; s < map.nsess; ++s) {
-        const int64_t last = map.visible[s] + T - 1;   // keys that the last token sees
-        const int64_t keys = last < map.n[s] ? (last > 0 ? last : 0) : map.n[s];
-        Span& sp = a.at.span[s];
-        sp.n = (int)map.n[s];
-        sp.visible = (int)map.visible[s];
-        sp.unit0 = (int)U;
-        sp.tiles = (int)((keys + kTile - 1) / kTile);
-        U += (int64_t)sp.tiles * Hkv * a.sets;
-        if (U > INT32_MAX / 32) return cudaErrorInvalidValue;   // unit and chunk numbers are 32 bits
-        shared = shared || sp.tiles != 1;
-    }
-    a.at.each = (int)U;
-    if (U > 0) {
+    const int units = lay_out(a, 1024);
+    if (units < 0) return cudaErrorInvalidValue;
+    if (units > 0) {
         cudaError_t e;
         switch (d) {
-            case 32: e = launch_dim<32>(nt, a); break;
-            case 64: e = launch_dim<64>(nt, a); break;
-            case 128: e = launch_dim<128>(nt, a); break;
-            case 256: e = launch_dim<256>(nt, a); break;
+            case 32: e = launch_dim<32>(nt, a, units); break;
+            case 64: e = launch_dim<64>(nt, a, units); break;
+            case 128: e = launch_dim<128>(nt, a, units); break;
+            case 256: e = launch_dim<256>(nt, a, units); break;
             default: return cudaErrorInvalidValue;
         }
-        if (e != cudaSuccess || !shared) return e;
+        if (e != cudaSuccess || !a.shared) return e;
     }
     return launch_ex(store_attend_merge_kernel, dim3((unsigned)((int64_t)map.nsess * Hkv * a.sets * pairs)),
                      dim3(kMergeThreads), 0, stream, a.P > 0, 1, a.at, a.slots, T, Hq, Hkv, a.sets, pairs, d, out, parts);

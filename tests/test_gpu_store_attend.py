@@ -384,3 +384,47 @@ def test_refusals():
         F.store_attend_batched([ks], [vs, vs], q[None, None])
     with pytest.raises(F.FathomError):
         F.store_attend_batched([ks] * 65, [vs] * 65, q[None, None].repeat(65, 1, 1, 1))
+
+
+@pytest.mark.parametrize("d,G,T,dtype", [(32, 2, 1, torch.float32), (64, 8, 1, torch.bfloat16), (128, 4, 1, torch.bfloat16),
+                                         (128, 1, 6, torch.float32), (256, 4, 1, torch.bfloat16),
+                                         (256, 8, 1, torch.float32), (64, 4, 3, torch.bfloat16)])
+def test_keys_for_the_whole_gpu(d, G, T, dtype):
+    """More 1024-key tiles than SMs: the long tiles, runs that end inside a row, rows of several CTAs."""
+    n, Hkv = 20000 + d, 8
+    ks, vs = make_store(n, Hkv, d, d + T), make_store(n, Hkv, d, d + 1)
+    q = queries((T, Hkv * G, d), d, dtype)
+    ref, tol, _, _ = reference(ks, vs, q, n - T + 1)
+    check(F.store_attend(ks, vs, q), ref, tol)
+
+
+@pytest.mark.parametrize("d,G,T,dtype", [(32, 1, 1, torch.bfloat16), (64, 8, 2, torch.float32), (128, 8, 1, torch.bfloat16),
+                                         (256, 2, 3, torch.bfloat16), (256, 4, 1, torch.float32)])
+def test_batched_shapes(d, G, T, dtype):
+    """Short sessions beside longer ones, in the batched call's tiles: ends of blocks, of warps' shares and of tiles."""
+    lens = [63, 1, 1000, 0, 65, 1025, 128, 2049, 3]
+    ks = [make_store(n, 2, d, 200 + i) for i, n in enumerate(lens)]
+    vs = [make_store(n, 2, d, 300 + i, capacity=n + 2000, garbage=True) for i, n in enumerate(lens)]
+    q = queries((len(lens), T, 2 * G, d), d, dtype)
+    out = F.store_attend_batched(ks, vs, q)
+    for s, n in enumerate(lens):
+        ref, tol, _, _ = reference(ks[s], vs[s], q[s], n - T + 1)
+        check(out[s], ref, tol)
+
+
+def test_back_to_back_calls_in_one_workspace():
+    """Calls of different shapes that follow each other in a stream share a workspace: each waits for the one before."""
+    shapes = [(300001, 1, 64, 4), (900, 2, 128, 4), (20000, 8, 128, 8), (100, 1, 256, 1)]
+    items = []
+    for i, (n, Hkv, d, G) in enumerate(shapes):
+        ks, vs, q = make_store(n, Hkv, d, 400 + i), make_store(n, Hkv, d, 500 + i), queries((Hkv * G, d), 400 + i)
+        items.append((ks, vs, q, F.store_attend(ks, vs, q)))
+    torch.cuda.synchronize()
+    nb = max(F.store_attend_workspace_bytes(k, 1, 1, q.shape[0]) for k, _, q, _ in items)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    for _ in range(10):
+        got = [F.store_attend(k, v, q, workspace=ws) for k, v, q, _ in items]
+        torch.cuda.synchronize()
+        for g, (_, _, _, want) in zip(got, items):
+            assert torch.equal(g, want)
+    assert F.last_device_status() == 0
