@@ -616,6 +616,8 @@ int store_attend(const fathom_store* Ks, const fathom_store* Vs, int S, const vo
         m.visible[e] = vis;
         m.nsess = e + 1;
     }
+    for (int i = 0; i * kAttendSets < S; ++i)
+        if (!store_attend_fits(maps[i], Hkv, T, Hq)) return FATHOM_EUNSUPPORTED;
     if (!is_here(q) || !is_here(dst) || !is_here(ws)) return FATHOM_EINVAL;
     if (!device_status_ptr()) return FATHOM_ECUDA;
     const size_t rows = (size_t)kAttendSets * T * Hq;   // of a group

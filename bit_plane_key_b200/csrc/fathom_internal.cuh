@@ -217,6 +217,8 @@ struct AttendMap {
     int64_t visible[kAttendSets];
 };
 size_t store_attend_workspace_bytes(int S, int T, int Hq, int Hkv, int d);
+// unit, chunk and row numbers of the launch fit 32 bits
+bool store_attend_fits(const AttendMap& map, int Hkv, int T, int Hq);
 // parts non-null: per-row partials [S][T][Hq][d + 2] instead of out
 cudaError_t launch_store_attend(const AttendMap& map, int Hkv, int d, const void* q, int q_dtype, int T, int Hq, float* out,
                                 float* parts, void* ws, cudaStream_t stream);

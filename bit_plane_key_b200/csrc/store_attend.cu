@@ -43,7 +43,7 @@ constexpr int kWarps = 8;                       // of a CTA
 constexpr int kThreads = 32 * kWarps;
 
 // NB: blocks of a warp
-template <int D, int NT, bool F32, int NB>
+template <int D, int NT, int NB>
 struct Shape {
     static constexpr int kTileBlocks = kWarps * NB, kTile = kTileBlocks * kBlock;
     static constexpr int kRow = kTileBlocks * 2;            // words of a plane row of the tile: 128 bytes, or 64
@@ -58,11 +58,10 @@ struct Shape {
     static constexpr int kRing = 4;
     static constexpr int kCodes = NB * CH * 8;              // words of a warp's codes of a chunk
     static constexpr int kOwn = kCodes > kPairs * D ? kCodes : kPairs * D;   // or of its partial outputs
-    static constexpr int kScales = 2 * NB * D;              // halves: K, V; block; channels, pair by pair
-    static constexpr int kQWords = NT * KS * 32 * 4;        // a lane's share of the queries
-    static constexpr int kQ2Words = F32 ? kQWords / 2 : 0;
+    static constexpr int kScales = 3 * NB * D;              // halves: K as floats, V; block; channels, pair by pair
+    static constexpr int kQWords = NT * KS * 64;            // [NT][ks][query][16 channels]
     static constexpr size_t kBytes = 4 * (size_t)(kRing * kRaw + kWarps * kOwn) + 2 * (size_t)(kWarps * kScales + 2 * kRawScales) +
-                                     4 * (size_t)(kQWords + kQ2Words) + 4 * (size_t)(2 * kWarps * kPairs + kPairs) +
+                                     4 * (size_t)kQWords + 4 * (size_t)(2 * kWarps * kPairs + kPairs) +
                                      8 * 2 * (kRing + 1);
     static constexpr size_t kSmem = kBytes + 1024;          // the planes start on a 1024-byte boundary
     static_assert(NB == 1 || NB == 2, "");
@@ -133,9 +132,6 @@ __device__ __forceinline__ uint32_t half2_of(float low, float high) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
     return r;
 }
-// the leading 11 significant bits
-__device__ __forceinline__ float leading11(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFFE000u); }
-
 // x where mask has a bit, else y; one instruction, where the expression takes two
 __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y, uint32_t mask) {
     uint32_t r;
@@ -247,12 +243,12 @@ __device__ __noinline__ Row row_of(const Spans<S>& m, int u, int Hkv, int sets) 
     return r;
 }
 
-template <int D, int NT, bool F32, int NS, int NB>
-__global__ void __launch_bounds__(kThreads, (Shape<D, NT, F32, NB>::kCtas))
+template <int D, int NT, int NS, int NB>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT, NB>::kCtas))
 store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __restrict__ q, int q_dtype, int T, int Hq,
                     int Hkv, int sets, float* __restrict__ slots, float* __restrict__ out, float* __restrict__ parts,
                     unsigned int* status) {
-    using Sh = Shape<D, NT, F32, NB>;
+    using Sh = Shape<D, NT, NB>;
     constexpr int kTile = Sh::kTile;
     constexpr int KS = Sh::KS, CH = Sh::CH, CK = Sh::CK, NC = Sh::NC, HP = Sh::HP, kPairs = Sh::kPairs, kRing = Sh::kRing;
     extern __shared__ uint32_t smem_raw[];
@@ -260,10 +256,9 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
     // [ring][plane][channel][row of the tile], 16-byte pieces swizzled by the channel
     uint32_t* s_codes = s_raw + kRing * Sh::kRaw;       // [warp][block][ks][lane][4] code words
     uint16_t* s_rs = reinterpret_cast<uint16_t*>(s_codes + kWarps * Sh::kOwn);     // [K, V][D][blocks of the tile] scales, the 16-byte pieces of 32 swizzled by the channel's bit 2
-    uint16_t* s_sc = s_rs + 2 * Sh::kRawScales;         // [warp][K, V][block][D] scales, K's times the block's factor
-    uint32_t* s_q = reinterpret_cast<uint32_t*>(s_sc + kWarps * Sh::kScales);      // [NT][ks][lane][4]
-    uint32_t* s_q2 = s_q + Sh::kQWords;                 // [NT][ks][lane][2], f32 queries only
-    float* s_m = reinterpret_cast<float*>(s_q2 + Sh::kQ2Words);   // [warp][pair]
+    uint16_t* s_sc = s_rs + 2 * Sh::kRawScales;         // [warp] K scales [block][D] as floats, times the block's factor; V scales [block][D]
+    float* s_q = reinterpret_cast<float*>(s_sc + kWarps * Sh::kScales);   // [NT][ks][query][16 channels], pair by pair
+    float* s_m = s_q + Sh::kQWords;                     // [warp][pair]
     float* s_l = s_m + kWarps * kPairs;
     float* s_f = s_l + kWarps * kPairs;                 // [pair] the query's part of the logits' factor
     uint64_t* s_full = reinterpret_cast<uint64_t*>(s_f + kPairs);   // [ring] the chunk has arrived; then the scales
@@ -309,7 +304,11 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
     pdl_wait();
     bool stuck = false;
     uint32_t* codes = s_codes + wp * Sh::kOwn;
-    uint16_t* scales = s_sc + wp * Sh::kScales;
+    float* k_scales = reinterpret_cast<float*>(s_sc + wp * Sh::kScales);
+    uint16_t* v_scales = s_sc + wp * Sh::kScales + 2 * NB * D;
+    // this lane's column of Q': the high half of its query, or (odd) the low one
+    const float2 high = (lg & 1) ? make_float2(-1.0f, -1.0f) : make_float2(1.0f, 1.0f);
+    const float2 low = (lg & 1) ? make_float2(1.0f, 1.0f) : make_float2(0.0f, 0.0f);
     int u = 0, j = 0;
     while (u < units) {
         const int s = rw.s;
@@ -317,9 +316,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         const bool whole = ub + u == rw.u0 && left <= units;   // no other CTA has a share of this row
         const int n = map.at.span[s].n, visible = map.at.span[s].visible;
 
-        // the set's queries in fp16, each scaled by a power of two to at most 2^6 to 2^7
-        // in magnitude (so that the least fp16 is 2^-31 of it): q1 = the value's first
-        // 11 bits, for f32 queries q2 = the next 11
+        // the set's queries, each scaled to a largest magnitude of 127
         for (int x = wp; x < kPairs; x += kWarps) {
             const int pr = rw.set * kPairs + x;
             float v[D / 32];
@@ -331,31 +328,15 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            // 2^-120 and below count as 0
-            const int ex = max((int)(__float_as_uint(mx) >> 23) - 133, -126);
-            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+            mx = fmaxf(mx, 1e-30f);                     // smaller queries than that count as 0 in part
+            const float down = 127.0f / mx;
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
                 const int c = paired<CH>(32 * e + lane);
-                const float vn = v[e] * down;
-                const __half q1 = __float2half_rn(vn);
-                // columns 2x and 2x + 1 of the 8; for the latter the operand is q1 d - rn(q1 d)
-                const int base = ((x >> 2) * KS + (c >> 4)) * 32 + (x & 3) * 8 + ((c >> 2) & 3);   // lane of column 2x
-                __half* h0 = reinterpret_cast<__half*>(s_q + base * 4) + (c & 3);
-                __half* h1 = h0 + 4 * 8;
-                h0[0] = q1;
-                h0[4] = __float2half_rn(0.0f);
-                h1[0] = __hneg(q1);
-                h1[4] = q1;
-                if (F32) {
-                    __half* g0 = reinterpret_cast<__half*>(s_q2 + base * 2) + (c & 3);
-                    g0[0] = __float2half_rn(0.0f);
-                    g0[4 * 4] = __float2half_rn(vn - __half2float(q1));
-                }
+                s_q[((x >> 2) * KS + (c >> 4)) * 64 + (x & 3) * 16 + (c & 15)] = v[e] * down;
             }
-            // logits in log2 units = sums of products * this * 2^24 / the block's factor;
-            // never 0, which a masked score of -inf would turn into NaN
-            if (lane == 0) s_f[x] = fmaxf(1.4426950408889634f / sqrtf((float)D) * __uint_as_float((uint32_t)(127 + ex) << 23), 1.17549435e-38f);
+            // logits in log2 units = sums of products * this * 2^24 * the block's factor
+            if (lane == 0) s_f[x] = 1.4426950408889634f / sqrtf((float)D) / 127.0f * mx;
         }
 
         float O[NT][KS][2], m[NT], l[NT];
@@ -401,36 +382,36 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                     const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&mh), o);
                     mh = __hmax2(mh, as_half2(other));
                 }
-                // a power of two sc keeps Q' inside fp16: the block's largest scale times it is
-                // in [2^6, 2^7) (or sc is 2^15, the largest factor in fp16: Q' then has 22 bits
-                // below its largest still)
+                // the block's largest scale goes to 127, so that |q Delta| < 2^14 (an f16 is 0 or at least 2^-24)
                 float sc[2] = {1.0f, 1.0f};
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const float dm = b ? __high2float(mh) : __low2float(mh);
-                    const int ex = max((int)(__float_as_uint(dm) >> 23), 118);
-                    sc[b] = __uint_as_float((uint32_t)(260 - ex) << 23);
-                    back[b] = __uint_as_float((uint32_t)(ex + 18) << 23);   // 2^24 / sc
+                    const float dm = fmaxf(b ? __high2float(mh) : __low2float(mh), 0x1p-24f);
+                    sc[b] = 127.0f / dm;
+                    back[b] = dm * (0x1p24f / 127.0f);
                 }
-                const __half2 sc2 = __floats2half2_rn(sc[0], sc[1]);
 #pragma unroll
                 for (int i = 0; i < 2 * D / 32; ++i) {
-                    __half2 v = as_half2(sw[i]);
-                    if (i < D / 32) v = __hmul2(v, sc2);
-                    __half* dst = reinterpret_cast<__half*>(scales) + (i < D / 32 ? 0 : NB * D) + paired<CH>(32 * (i % (D / 32)) + lane);
-                    dst[0] = __low2half(v);
-                    if (NB == 2) dst[D] = __high2half(v);
+                    const __half2 v = as_half2(sw[i]);
+                    const int c = paired<CH>(32 * (i % (D / 32)) + lane);
+                    if (i < D / 32) {
+                        k_scales[c] = __low2float(v) * sc[0];
+                        if (NB == 2) k_scales[D + c] = __high2float(v) * sc[1];
+                    } else {
+                        v_scales[c] = (uint16_t)sw[i];
+                        if (NB == 2) v_scales[D + c] = (uint16_t)(sw[i] >> 16);
+                    }
                 }
             }
             // scores of 16-key tiles p; then, in [p][0] and [p][1], the bits of their weights as operands
-            float S[NB][NT][4][4], B15[NB][NT][4], neg[NB][NT];
+            float S[NB][NT][4][4], B15[NB][NT][4], neg[NB][NT][2];
             // the lane's channel pair, and its block (of two) or word (of one block)
             const int pl = NB == 2 ? (lane & 7) + 8 * (lane >> 4) : lane >> 1, part = NB == 2 ? (lane >> 3) & 1 : lane & 1;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    neg[b][nt] = 0.0f;
+                    neg[b][nt][0] = neg[b][nt][1] = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         B15[b][nt][e] = 0.0f;
@@ -532,29 +513,21 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                     for (int k = 0; k < CK; ++k) {
                         const int ks = c * CK + k;
                         uint32_t bq[NB][NT][2];
-                        __half2 da[NB], db[NB];
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            const uint2 d4 = *reinterpret_cast<const uint2*>(scales + b * D + 16 * ks + 4 * lt);
-                            da[b] = as_half2(d4.x);
-                            db[b] = as_half2(d4.y);
-                        }
+                            const float4 d4 = *reinterpret_cast<const float4*>(k_scales + b * D + 16 * ks + 4 * lt);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint4 q4 = *reinterpret_cast<const uint4*>(s_q + ((nt * KS + ks) * 32 + lane) * 4);
-                            uint2 q2 = make_uint2(0u, 0u);
-                            if (F32) q2 = *reinterpret_cast<const uint2*>(s_q2 + ((nt * KS + ks) * 32 + lane) * 2);
-#pragma unroll
-                            for (int b = 0; b < NB; ++b) {
-                                // even column: z = rn(q1 d); odd: z = q1 d - rn(q1 d), exact, + q2 d
-                                __half2 za = __hfma2(as_half2(q4.z), da[b], __hmul2_rn(as_half2(q4.x), da[b]));
-                                __half2 zb = __hfma2(as_half2(q4.w), db[b], __hmul2_rn(as_half2(q4.y), db[b]));
-                                if (F32) {
-                                    za = __hfma2(as_half2(q2.x), da[b], za);
-                                    zb = __hfma2(as_half2(q2.y), db[b], zb);
-                                }
-                                bq[b][nt][0] = *reinterpret_cast<const uint32_t*>(&za);
-                                bq[b][nt][1] = *reinterpret_cast<const uint32_t*>(&zb);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                // v = q Delta; its high half is rounded to a multiple of 8 (the sum with 1.5 2^26 is)
+                                const float4 q4 = *reinterpret_cast<const float4*>(s_q + (nt * KS + ks) * 64 + (lg >> 1) * 16 + 4 * lt);
+                                const float2 va = __fmul2_rn(make_float2(q4.x, q4.y), make_float2(d4.x, d4.y));
+                                const float2 vb = __fmul2_rn(make_float2(q4.z, q4.w), make_float2(d4.z, d4.w));
+                                const float2 up = make_float2(0x1.8p26f, 0x1.8p26f), down = make_float2(-0x1.8p26f, -0x1.8p26f);
+                                const float2 ha = __fadd2_rn(__fadd2_rn(va, up), down), hb = __fadd2_rn(__fadd2_rn(vb, up), down);
+                                const float2 za = __ffma2_rn(ha, high, __fmul2_rn(va, low));
+                                const float2 zb = __ffma2_rn(hb, high, __fmul2_rn(vb, low));
+                                bq[b][nt][0] = half2_of(za.x, za.y);
+                                bq[b][nt][1] = half2_of(zb.x, zb.y);
                                 mma(B15[b][nt], a15, bq[b][nt]);
                             }
                         }
@@ -579,18 +552,18 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float f = s_f[nt * kTilePairs + lt];
-                        float F[NB];
+                        float F[NB], top[NB];
                         float mn = m[nt];
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            const float off = -0.5f * (B15[b][nt][0] + B15[b][nt][1]);
                             float mx = -INFINITY;
 #pragma unroll
                             for (int p = 0; p < 4; ++p) {
                                 const float un = (p & 1) ? 0.0625f : 1.0f;
                                 float* v = S[b][nt][p];
-                                v[0] = fmaf(v[0] + v[1], un, off);
-                                v[2] = fmaf(v[2] + v[3], un, off);
+                                // the high halves' sums, and their offset, are exact
+                                v[0] = fmaf(v[0], un, -0.5f * B15[b][nt][0]) + fmaf(v[1], un, -0.5f * B15[b][nt][1]);
+                                v[2] = fmaf(v[2], un, -0.5f * B15[b][nt][0]) + fmaf(v[3], un, -0.5f * B15[b][nt][1]);
                                 if (cut) {
                                     const int key = k0 + b * kBlock + 4 * (p + 4 * (lg & 1)) + (lg >> 1);
                                     if (key >= limit[nt]) v[0] = -INFINITY;
@@ -599,10 +572,12 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                                 mx = fmaxf(mx, fmaxf(v[0], v[2]));
                             }
                             F[b] = f * back[b];
-                            mn = fmaxf(mn, mx * F[b]);
-                        }
 #pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                            top[b] = mx * F[b];
+                            // a whole number: what was summed so far is rescaled by powers of two, exactly
+                            mn = fmaxf(mn, ceilf(top[b]));
+                        }
                         const float base = mn == -INFINITY ? 0.0f : mn;
                         // S F - base is rounded once; where the product's own rounding exceeds
                         // the exponents that matter, both are rounded alike instead
@@ -621,18 +596,22 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                         moved |= mn != m[nt];
                         m[nt] = mn;
 #pragma unroll
-                        for (int b = 0; b < NB; ++b)
+                        for (int b = 0; b < NB; ++b) {
+                            // the high halves of a block's weights are multiples of 2^-11 of (the power of two above)
+                            // the largest: P + round is rounded to one
+                            const float round = __uint_as_float(__float_as_uint(ex2(top[b] - base)) & 0x7F800000u) * 0x1.8p28f;
 #pragma unroll
                             for (int p = 0; p < 4; ++p) {
                                 // weights times 2^15, or 2^11 where the codes come 16 times as large
-                                const float up = (p & 1) ? 2048.0f : 32768.0f;
+                                const float up = (p & 1) ? 2048.0f : 32768.0f, r = (p & 1) ? round * 0.0625f : round;
 #pragma unroll
                                 for (int w = 0; w < 2; ++w) {
                                     const float v = ex2(fmaf(S[b][nt][p][2 * w], F[b], -base)) * up;
-                                    const float h = leading11(v);
+                                    const float h = __fadd_rn(__fadd_rn(v, r), -r);
                                     S[b][nt][p][w] = __uint_as_float(transpose8x8(half2_of(h, v - h)));
                                 }
                             }
+                        }
                     }
                     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -656,9 +635,9 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                                 const uint32_t v15 = (p & 1) ? 0x00F000F0u : 0x000F000Fu, a[4] = {v15, v15, v15, v15};
                                 mma_p(c4, a, S[b][nt][p]);
                             }
-                            const float sum = c4[0] + c4[1];
-                            neg[b][nt] = -0.5f * sum;
-                            l[nt] = fmaf(sum, 512.0f / 15.0f, l[nt]);   // 2^24 / 2^15
+                            neg[b][nt][0] = -0.5f * c4[0];
+                            neg[b][nt][1] = -0.5f * c4[1];
+                            l[nt] = fmaf(c4[0] + c4[1], 512.0f / 15.0f, l[nt]);   // 2^24 / 2^15
                         }
             }
 #pragma unroll
@@ -676,7 +655,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                                 uint32_t a[4][4];
                                 operands(vc[b * (Sh::kCodes / (4 * NB)) + k * 32], a);
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) acc[b][nt][0] = acc[b][nt][2] = neg[b][nt], acc[b][nt][1] = acc[b][nt][3] = 0.0f;
+                                for (int nt = 0; nt < NT; ++nt) acc[b][nt][0] = acc[b][nt][2] = neg[b][nt][0], acc[b][nt][1] = acc[b][nt][3] = neg[b][nt][1];
 #pragma unroll
                                 for (int p = 0; p < 4; ++p)
 #pragma unroll
@@ -684,7 +663,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                             }
 #pragma unroll
                             for (int b = 0; b < NB; ++b) {
-                                const float2 dv = __half22float2(*reinterpret_cast<const __half2*>(scales + (NB + b) * D + 16 * mt + 2 * lg));
+                                const float2 dv = __half22float2(*reinterpret_cast<const __half2*>(v_scales + b * D + 16 * mt + 2 * lg));
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
                                     O[nt][mt][0] = fmaf(acc[b][nt][0] + acc[b][nt][1], dv.x, O[nt][mt][0]);
@@ -855,6 +834,15 @@ inline int tiles_of_set(int64_t C) { return C <= kTilePairs ? 1 : 2; }
 
 }  // namespace
 
+bool store_attend_fits(const AttendMap& map, int Hkv, int T, int Hq) {
+    const int64_t C = (int64_t)T * (Hq / Hkv);
+    const int pairs = tiles_of_set(C) * kTilePairs;
+    const int64_t rows = Hkv * ((C + pairs - 1) / pairs);   // of a session
+    int64_t units = 0;
+    for (int s = 0; s < map.nsess; ++s) units += (map.n[s] + 1023) / 1024 * rows;
+    return units <= INT32_MAX / 32 && map.nsess * rows * pairs <= INT32_MAX;
+}
+
 size_t store_attend_workspace_bytes(int S, int T, int Hq, int Hkv, int d) {
     const int64_t C = (int64_t)T * (Hq / Hkv);
     const int pairs = tiles_of_set(C) * kTilePairs;
@@ -904,7 +892,7 @@ bool tensor_maps(CUtensorMap* tm, CUtensorMap* stm, const uint32_t* planes, cons
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Lays the sessions out in tiles; the number of units, or -1 if unit and chunk numbers would not fit 32 bits.
+// Lays the sessions out in tiles; the number of units.
 int lay_out(Call& a, int tile) {
     int64_t U = 0;
     for (int s = 0; s < a.map.nsess; ++s) {
@@ -916,19 +904,17 @@ int lay_out(Call& a, int tile) {
         sp.unit0 = (int)U;
         sp.tiles = (int)((keys + tile - 1) / tile);
         U += (int64_t)sp.tiles * a.Hkv * a.sets;
-        if (U > INT32_MAX / 32) return -1;
         a.shared = a.shared || sp.tiles != 1;
     }
     return (int)U;
 }
 
-template <int D, int NT, bool F32, int NS, int NB>
+template <int D, int NT, int NS, int NB>
 cudaError_t launch_shape(Call& a) {
-    using Sh = Shape<D, NT, F32, NB>;
+    using Sh = Shape<D, NT, NB>;
     static_assert(Sh::kCtas * (Sh::kSmem + 1024) <= kMaxSmem + 1024, "the CTAs of an SM fit");
     a.shared = false;
     const int U = lay_out(a, Sh::kTile);
-    if (U < 0) return cudaErrorInvalidValue;
     a.P = U < 148 * Sh::kCtas ? U : 148 * Sh::kCtas;
     a.at.each = U / a.P;
     a.at.more = U % a.P;
@@ -942,27 +928,25 @@ cudaError_t launch_shape(Call& a) {
             !tensor_maps(&m.v[s], &m.vs[s], a.map.v_planes[s], a.map.v_scales[s], a.Hkv * D, D, a.map.v_pad[s], Sh::kTile))
             return cudaErrorInvalidValue;
     }
-    auto kern = store_attend_kernel<D, NT, F32, NS, NB>;
+    auto kern = store_attend_kernel<D, NT, NS, NB>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
     if (e != cudaSuccess) return e;
     return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, true, 1, m, a.q, a.q_dtype, a.T, a.Hq, a.Hkv,
                      a.sets, a.slots, a.out, a.parts, device_status_ptr());
 }
 
-template <int D, int NT, bool F32>
+template <int D, int NT>
 cudaError_t launch_type(Call& a, int units) {
-    if (a.at.nsess > 1) return launch_shape<D, NT, F32, kAttendSets, 2>(a);
+    if (a.at.nsess > 1) return launch_shape<D, NT, kAttendSets, 2>(a);
     // few keys: half as long tiles, as long as all run at once (1 head of 128, 4096 keys: 9.0 us against
     // 11.4; 2 heads of 256, 8 queries each, 70001 keys, whose half tiles would not: 36 us against 27)
-    if (2 * units <= 148 * Shape<D, NT, F32, 1>::kCtas) return launch_shape<D, NT, F32, 1, 1>(a);
-    return launch_shape<D, NT, F32, 1, 2>(a);
+    if (2 * units <= 148 * Shape<D, NT, 1>::kCtas) return launch_shape<D, NT, 1, 1>(a);
+    return launch_shape<D, NT, 1, 2>(a);
 }
 
 template <int D>
 cudaError_t launch_dim(int nt, Call& a, int units) {
-    const bool f32 = a.q_dtype == FATHOM_F32;
-    if (nt == 1) return f32 ? launch_type<D, 1, true>(a, units) : launch_type<D, 1, false>(a, units);
-    return f32 ? launch_type<D, 2, true>(a, units) : launch_type<D, 2, false>(a, units);
+    return nt == 1 ? launch_type<D, 1>(a, units) : launch_type<D, 2>(a, units);
 }
 
 }  // namespace
@@ -974,7 +958,6 @@ cudaError_t launch_store_attend(const AttendMap& map, int Hkv, int d, const void
     Call a{map, q, q_dtype, T, Hq, Hkv, (int)((C + pairs - 1) / pairs), static_cast<float*>(ws), out, parts, stream, {}, 0, false};
     a.at.nsess = map.nsess;
     const int units = lay_out(a, 1024);
-    if (units < 0) return cudaErrorInvalidValue;
     if (units > 0) {
         cudaError_t e;
         switch (d) {

@@ -473,15 +473,18 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
  *             host-resident; n may be 0.
  *   q         device, [n_tokens][Hq][d], FATHOM_F32 or FATHOM_BF16, finite values;
  *             1 <= n_tokens <= 4096 (made for few tokens: the stores are read again
- *             for every 16 (token, head of a group) pairs).
+ *             for every 8 (token, head of a group) pairs).
  *   out       device, f32 [n_tokens][Hq][d].
  *   workspace device, 256-byte aligned, fathom_store_attend_workspace_bytes() bytes;
  *             contents need not be initialised, and are free once the call's
  *             kernels are done.  Calls that overlap on the GPU need one each.
- * A call with the same arguments gives the same bits.
+ * A call with the same arguments gives the same bits.  The call's kernels are
+ * launched with programmatic serialization: they are scheduled while the kernel
+ * before them in the stream finishes, and wait for it before they read or write.
  * Errors: EINVAL for null pointers, bad sizes, stores that differ, arrays not on
  * this device or not where host_resident says; ENOMEM for a short workspace;
- * EUNSUPPORTED for d other than 32, 64, 128, 256.
+ * EUNSUPPORTED for d other than 32, 64, 128, 256, and for more work than 2^26
+ * tiles of 1024 keys for 8 pairs each.
  */
 size_t fathom_store_attend_workspace_bytes(int n_sessions, int n_tokens, int n_q_heads, int n_kv_heads, int d);
 int fathom_store_attend(const fathom_store* K, const fathom_store* V, const void* q, int q_dtype, int n_tokens,

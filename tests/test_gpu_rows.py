@@ -306,3 +306,52 @@ def test_a_layers_steps_together(interleaved):
     _, idx, _, out = F.decode_step(ks, q[0], s2, 92, 256, Kr, Vr)
     assert (idx >= 0).all() and (idx < n).all() and torch.isfinite(out).all()
     assert F.last_device_status() == 0
+
+
+def test_calls_behind_copies_memsets_and_other_streams():
+    """The calls follow whatever the stream holds, run or captured: a copy, a memset, a kernel of another library, work
+    joined from another stream."""
+    Hq, Hkv, d, n = 8, 2, 128, 700
+    g = torch.Generator(device=DEV).manual_seed(3)
+    qkv = torch.randn(3, Hq + 2 * Hkv, d, device=DEV, generator=g)
+    Kr, Vr = _row_cache(Hkv, n, d, True, 31)
+    inv = freqs(d)
+    K0, V0 = Kr.clone(), Vr.clone()
+    src = qkv.clone()
+
+    def step(side):
+        ks, vs = F.Store.empty(Hkv, d, n, device=DEV), F.Store.empty(Hkv, d, n, device=DEV)
+        buf = torch.empty_like(src)
+        buf.copy_(src)                                       # a copy, then the rotation
+        q = F.qk_norm_rope(buf, Hq, Hkv, inv, Kr, Vr, n - 3)
+        ks.planes.zero_(), vs.planes.zero_()                 # memsets, then the append
+        F.append_rows(ks, vs, Kr, Vr, n)
+        out = torch.empty(3, Hq, d, device=DEV)
+        ev = torch.cuda.Event()
+        ev.record()
+        with torch.cuda.stream(side):
+            ev.wait()
+            out.fill_(7.0)                                   # on the other stream, joined before the attention
+            ev2 = torch.cuda.Event()
+            ev2.record()
+        ev2.wait()
+        F.store_attend(ks, vs, q, out=out)
+        return q, ks, vs, out * 1.0                          # and another library's kernel behind it
+
+    side = torch.cuda.Stream()
+    q, ks, vs, out = step(side)
+    torch.cuda.synchronize()
+    assert torch.equal(Kr[:, :n - 3], K0[:, :n - 3]) and torch.equal(Vr[:, :n - 3], V0[:, :n - 3])
+    _same(ks, Kr, n)
+    _same(vs, Vr, n)
+    want, tol, _, _ = reference(ks, vs, q, n - 2)
+    check(out, want, tol)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q2, ks2, vs2, out2 = step(side)
+    for _ in range(3):
+        Kr[:, n - 3:] = 0
+        out2.zero_(), q2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out2, out) and torch.equal(q2, q) and torch.equal(ks2.planes, ks.planes)
