@@ -43,7 +43,7 @@ constexpr int kWarps = 8;                       // of a CTA
 constexpr int kThreads = 32 * kWarps;
 
 // NB: blocks of a warp
-template <int D, int NT, int NB>
+template <int D, int NT, bool F32, int NB>
 struct Shape {
     static constexpr int kTileBlocks = kWarps * NB, kTile = kTileBlocks * kBlock;
     static constexpr int kRow = kTileBlocks * 2;            // words of a plane row of the tile: 128 bytes, or 64
@@ -58,10 +58,11 @@ struct Shape {
     static constexpr int kRing = 4;
     static constexpr int kCodes = NB * CH * 8;              // words of a warp's codes of a chunk
     static constexpr int kOwn = kCodes > kPairs * D ? kCodes : kPairs * D;   // or of its partial outputs
-    static constexpr int kScales = 3 * NB * D;              // halves: K as floats, V; block; channels, pair by pair
-    static constexpr int kQWords = NT * KS * 64;            // [NT][ks][query][16 channels]
+    static constexpr int kScales = 2 * NB * D;              // halves: K, V; block; channels, pair by pair
+    static constexpr int kQWords = NT * KS * 32 * 4;        // a lane's share of the queries
+    static constexpr int kQ2Words = F32 ? kQWords / 2 : 0;
     static constexpr size_t kBytes = 4 * (size_t)(kRing * kRaw + kWarps * kOwn) + 2 * (size_t)(kWarps * kScales + 2 * kRawScales) +
-                                     4 * (size_t)kQWords + 4 * (size_t)(2 * kWarps * kPairs + kPairs) +
+                                     4 * (size_t)(kQWords + kQ2Words) + 4 * (size_t)(2 * kWarps * kPairs + kPairs) +
                                      8 * 2 * (kRing + 1);
     static constexpr size_t kSmem = kBytes + 1024;          // the planes start on a 1024-byte boundary
     static_assert(NB == 1 || NB == 2, "");
@@ -132,6 +133,20 @@ __device__ __forceinline__ uint32_t half2_of(float low, float high) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
     return r;
 }
+// Two values v = q Delta below 2^14, q = q1 + q2, as a column's operand.  Even column:
+// the high half h, v's whole number in 10 bits or more (the sum with 1536 of an fp16
+// up to 2^14 has no fraction).  Odd column: q1 Delta - h, rounded once, + q2 Delta.
+// Sums of the high halves' products with codes are whole numbers, too: the matrix
+// unit, which cuts addends off where fp32 would round a sum, adds them exactly
+// below 2^24, as it would not products of an fp16's full range.
+__device__ __forceinline__ uint32_t half_of_product(uint32_t q1, uint32_t own, uint32_t q2, uint32_t delta, __half2 sign, bool f32) {
+    const __half2 d = as_half2(delta), big = __float2half2_rn(1536.0f);
+    const __half2 h = __hadd2_rn(__hfma2(as_half2(q1), d, big), __hneg2(big));
+    __half2 z = __hfma2(as_half2(own), d, __hmul2_rn(h, sign));
+    if (f32) z = __hfma2(as_half2(q2), d, z);
+    return *reinterpret_cast<const uint32_t*>(&z);
+}
+
 // x where mask has a bit, else y; one instruction, where the expression takes two
 __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y, uint32_t mask) {
     uint32_t r;
@@ -243,12 +258,12 @@ __device__ __noinline__ Row row_of(const Spans<S>& m, int u, int Hkv, int sets) 
     return r;
 }
 
-template <int D, int NT, int NS, int NB>
-__global__ void __launch_bounds__(kThreads, (Shape<D, NT, NB>::kCtas))
+template <int D, int NT, bool F32, int NS, int NB>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT, F32, NB>::kCtas))
 store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __restrict__ q, int q_dtype, int T, int Hq,
                     int Hkv, int sets, float* __restrict__ slots, float* __restrict__ out, float* __restrict__ parts,
                     unsigned int* status) {
-    using Sh = Shape<D, NT, NB>;
+    using Sh = Shape<D, NT, F32, NB>;
     constexpr int kTile = Sh::kTile;
     constexpr int KS = Sh::KS, CH = Sh::CH, CK = Sh::CK, NC = Sh::NC, HP = Sh::HP, kPairs = Sh::kPairs, kRing = Sh::kRing;
     extern __shared__ uint32_t smem_raw[];
@@ -256,9 +271,10 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
     // [ring][plane][channel][row of the tile], 16-byte pieces swizzled by the channel
     uint32_t* s_codes = s_raw + kRing * Sh::kRaw;       // [warp][block][ks][lane][4] code words
     uint16_t* s_rs = reinterpret_cast<uint16_t*>(s_codes + kWarps * Sh::kOwn);     // [K, V][D][blocks of the tile] scales, the 16-byte pieces of 32 swizzled by the channel's bit 2
-    uint16_t* s_sc = s_rs + 2 * Sh::kRawScales;         // [warp] K scales [block][D] as floats, times the block's factor; V scales [block][D]
-    float* s_q = reinterpret_cast<float*>(s_sc + kWarps * Sh::kScales);   // [NT][ks][query][16 channels], pair by pair
-    float* s_m = s_q + Sh::kQWords;                     // [warp][pair]
+    uint16_t* s_sc = s_rs + 2 * Sh::kRawScales;         // [warp][K, V][block][D] scales, K's times the block's factor
+    uint32_t* s_q = reinterpret_cast<uint32_t*>(s_sc + kWarps * Sh::kScales);      // [NT][ks][lane][4]
+    uint32_t* s_q2 = s_q + Sh::kQWords;                 // [NT][ks][lane][2], f32 queries only
+    float* s_m = reinterpret_cast<float*>(s_q2 + Sh::kQ2Words);   // [warp][pair]
     float* s_l = s_m + kWarps * kPairs;
     float* s_f = s_l + kWarps * kPairs;                 // [pair] the query's part of the logits' factor
     uint64_t* s_full = reinterpret_cast<uint64_t*>(s_f + kPairs);   // [ring] the chunk has arrived; then the scales
@@ -304,11 +320,8 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
     pdl_wait();
     bool stuck = false;
     uint32_t* codes = s_codes + wp * Sh::kOwn;
-    float* k_scales = reinterpret_cast<float*>(s_sc + wp * Sh::kScales);
-    uint16_t* v_scales = s_sc + wp * Sh::kScales + 2 * NB * D;
-    // this lane's column of Q': the high half of its query, or (odd) the low one
-    const float2 high = (lg & 1) ? make_float2(-1.0f, -1.0f) : make_float2(1.0f, 1.0f);
-    const float2 low = (lg & 1) ? make_float2(1.0f, 1.0f) : make_float2(0.0f, 0.0f);
+    uint16_t *k_scales = s_sc + wp * Sh::kScales, *v_scales = k_scales + NB * D;
+    const __half2 sign = __float2half2_rn((lg & 1) ? -1.0f : 1.0f);   // of Q's high half in this lane's column
     int u = 0, j = 0;
     while (u < units) {
         const int s = rw.s;
@@ -316,7 +329,9 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         const bool whole = ub + u == rw.u0 && left <= units;   // no other CTA has a share of this row
         const int n = map.at.span[s].n, visible = map.at.span[s].visible;
 
-        // the set's queries, each scaled to a largest magnitude of 127
+        // the set's queries in fp16, each scaled by a power of two to at most 2^6 to 2^7
+        // in magnitude (so that the least fp16 is 2^-31 of it): q1 = the value's first
+        // 11 bits, for f32 queries q2 = the next 11
         for (int x = wp; x < kPairs; x += kWarps) {
             const int pr = rw.set * kPairs + x;
             float v[D / 32];
@@ -328,15 +343,29 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx = fmaxf(mx, 1e-30f);                     // smaller queries than that count as 0 in part
-            const float down = 127.0f / mx;
+            // 2^-120 and below count as 0
+            const int ex = max((int)(__float_as_uint(mx) >> 23) - 133, -126);
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
                 const int c = paired<CH>(32 * e + lane);
-                s_q[((x >> 2) * KS + (c >> 4)) * 64 + (x & 3) * 16 + (c & 15)] = v[e] * down;
+                const float vn = v[e] * down;
+                const __half q1 = __float2half_rn(vn), none = __float2half_rn(0.0f);
+                // columns 2x and 2x + 1 of the 8: q1 of both, then what the column's operand is made of, none and q1
+                const int base = ((x >> 2) * KS + (c >> 4)) * 32 + (x & 3) * 8 + ((c >> 2) & 3);   // lane of column 2x
+                __half* h0 = reinterpret_cast<__half*>(s_q + base * 4) + (c & 3);
+                __half* h1 = h0 + 4 * 8;
+                h0[0] = h1[0] = h1[4] = q1;
+                h0[4] = none;
+                if (F32) {
+                    __half* g0 = reinterpret_cast<__half*>(s_q2 + base * 2) + (c & 3);
+                    g0[0] = none;
+                    g0[4 * 4] = __float2half_rn(vn - __half2float(q1));
+                }
             }
-            // logits in log2 units = sums of products * this * 2^24 * the block's factor
-            if (lane == 0) s_f[x] = 1.4426950408889634f / sqrtf((float)D) / 127.0f * mx;
+            // logits in log2 units = sums of products * this * 2^24 / the block's factor;
+            // never 0, which a masked score of -inf would turn into NaN
+            if (lane == 0) s_f[x] = fmaxf(1.4426950408889634f / sqrtf((float)D) * __uint_as_float((uint32_t)(127 + ex) << 23), 1.17549435e-38f);
         }
 
         float O[NT][KS][2], m[NT], l[NT];
@@ -382,25 +411,23 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                     const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&mh), o);
                     mh = __hmax2(mh, as_half2(other));
                 }
-                // the block's largest scale goes to 127, so that |q Delta| < 2^14 (an f16 is 0 or at least 2^-24)
+                // a power of two sc brings the block's largest scale to [2^6, 2^7), so that |q Delta| < 2^14
+                // (an f16 is 0 or at least 2^-24)
                 float sc[2] = {1.0f, 1.0f};
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const float dm = fmaxf(b ? __high2float(mh) : __low2float(mh), 0x1p-24f);
-                    sc[b] = 127.0f / dm;
-                    back[b] = dm * (0x1p24f / 127.0f);
+                    const float dm = b ? __high2float(mh) : __low2float(mh);
+                    const int ex = max((int)(__float_as_uint(dm) >> 23), 103);
+                    sc[b] = __uint_as_float((uint32_t)(260 - ex) << 23);
+                    back[b] = __uint_as_float((uint32_t)(ex + 18) << 23);   // 2^24 / sc
                 }
 #pragma unroll
                 for (int i = 0; i < 2 * D / 32; ++i) {
-                    const __half2 v = as_half2(sw[i]);
-                    const int c = paired<CH>(32 * (i % (D / 32)) + lane);
-                    if (i < D / 32) {
-                        k_scales[c] = __low2float(v) * sc[0];
-                        if (NB == 2) k_scales[D + c] = __high2float(v) * sc[1];
-                    } else {
-                        v_scales[c] = (uint16_t)sw[i];
-                        if (NB == 2) v_scales[D + c] = (uint16_t)(sw[i] >> 16);
-                    }
+                    __half2 v = as_half2(sw[i]);
+                    if (i < D / 32) v = __floats2half2_rn(__low2float(v) * sc[0], __high2float(v) * sc[1]);
+                    __half* dst = reinterpret_cast<__half*>(i < D / 32 ? k_scales : v_scales) + paired<CH>(32 * (i % (D / 32)) + lane);
+                    dst[0] = __low2half(v);
+                    if (NB == 2) dst[D] = __high2half(v);
                 }
             }
             // scores of 16-key tiles p; then, in [p][0] and [p][1], the bits of their weights as operands
@@ -514,20 +541,15 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                         const int ks = c * CK + k;
                         uint32_t bq[NB][NT][2];
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            const float4 d4 = *reinterpret_cast<const float4*>(k_scales + b * D + 16 * ks + 4 * lt);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint4 q4 = *reinterpret_cast<const uint4*>(s_q + ((nt * KS + ks) * 32 + lane) * 4);
+                            uint2 q2 = make_uint2(0u, 0u);
+                            if (F32) q2 = *reinterpret_cast<const uint2*>(s_q2 + ((nt * KS + ks) * 32 + lane) * 2);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                // v = q Delta; its high half is rounded to a multiple of 8 (the sum with 1.5 2^26 is)
-                                const float4 q4 = *reinterpret_cast<const float4*>(s_q + (nt * KS + ks) * 64 + (lg >> 1) * 16 + 4 * lt);
-                                const float2 va = __fmul2_rn(make_float2(q4.x, q4.y), make_float2(d4.x, d4.y));
-                                const float2 vb = __fmul2_rn(make_float2(q4.z, q4.w), make_float2(d4.z, d4.w));
-                                const float2 up = make_float2(0x1.8p26f, 0x1.8p26f), down = make_float2(-0x1.8p26f, -0x1.8p26f);
-                                const float2 ha = __fadd2_rn(__fadd2_rn(va, up), down), hb = __fadd2_rn(__fadd2_rn(vb, up), down);
-                                const float2 za = __ffma2_rn(ha, high, __fmul2_rn(va, low));
-                                const float2 zb = __ffma2_rn(hb, high, __fmul2_rn(vb, low));
-                                bq[b][nt][0] = half2_of(za.x, za.y);
-                                bq[b][nt][1] = half2_of(zb.x, zb.y);
+                            for (int b = 0; b < NB; ++b) {
+                                const uint2 d4 = *reinterpret_cast<const uint2*>(k_scales + b * D + 16 * ks + 4 * lt);
+                                bq[b][nt][0] = half_of_product(q4.x, q4.z, q2.x, d4.x, sign, F32);
+                                bq[b][nt][1] = half_of_product(q4.y, q4.w, q2.y, d4.y, sign, F32);
                                 mma(B15[b][nt], a15, bq[b][nt]);
                             }
                         }
@@ -909,9 +931,9 @@ int lay_out(Call& a, int tile) {
     return (int)U;
 }
 
-template <int D, int NT, int NS, int NB>
+template <int D, int NT, bool F32, int NS, int NB>
 cudaError_t launch_shape(Call& a) {
-    using Sh = Shape<D, NT, NB>;
+    using Sh = Shape<D, NT, F32, NB>;
     static_assert(Sh::kCtas * (Sh::kSmem + 1024) <= kMaxSmem + 1024, "the CTAs of an SM fit");
     a.shared = false;
     const int U = lay_out(a, Sh::kTile);
@@ -928,25 +950,27 @@ cudaError_t launch_shape(Call& a) {
             !tensor_maps(&m.v[s], &m.vs[s], a.map.v_planes[s], a.map.v_scales[s], a.Hkv * D, D, a.map.v_pad[s], Sh::kTile))
             return cudaErrorInvalidValue;
     }
-    auto kern = store_attend_kernel<D, NT, NS, NB>;
+    auto kern = store_attend_kernel<D, NT, F32, NS, NB>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
     if (e != cudaSuccess) return e;
     return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, true, 1, m, a.q, a.q_dtype, a.T, a.Hq, a.Hkv,
                      a.sets, a.slots, a.out, a.parts, device_status_ptr());
 }
 
-template <int D, int NT>
+template <int D, int NT, bool F32>
 cudaError_t launch_type(Call& a, int units) {
-    if (a.at.nsess > 1) return launch_shape<D, NT, kAttendSets, 2>(a);
+    if (a.at.nsess > 1) return launch_shape<D, NT, F32, kAttendSets, 2>(a);
     // few keys: half as long tiles, as long as all run at once (1 head of 128, 4096 keys: 9.0 us against
     // 11.4; 2 heads of 256, 8 queries each, 70001 keys, whose half tiles would not: 36 us against 27)
-    if (2 * units <= 148 * Shape<D, NT, 1>::kCtas) return launch_shape<D, NT, 1, 1>(a);
-    return launch_shape<D, NT, 1, 2>(a);
+    if (2 * units <= 148 * Shape<D, NT, F32, 1>::kCtas) return launch_shape<D, NT, F32, 1, 1>(a);
+    return launch_shape<D, NT, F32, 1, 2>(a);
 }
 
 template <int D>
 cudaError_t launch_dim(int nt, Call& a, int units) {
-    return nt == 1 ? launch_type<D, 1>(a, units) : launch_type<D, 2>(a, units);
+    const bool f32 = a.q_dtype == FATHOM_F32;
+    if (nt == 1) return f32 ? launch_type<D, 1, true>(a, units) : launch_type<D, 1, false>(a, units);
+    return f32 ? launch_type<D, 2, true>(a, units) : launch_type<D, 2, false>(a, units);
 }
 
 }  // namespace

@@ -428,3 +428,18 @@ def test_back_to_back_calls_in_one_workspace():
         for g, (_, _, _, want) in zip(got, items):
             assert torch.equal(g, want)
     assert F.last_device_status() == 0
+
+
+@pytest.mark.parametrize("n,d,G", [(131072, 64, 4), (60000, 128, 8), (4000, 256, 2)])
+def test_long_sums_are_not_biased(n, d, G):
+    """Flat weights over many keys: outputs are small beside the values, so an error that every block makes alike would show.
+    The errors of the weights are independent and of both signs: of a logit, 2^-21 / sqrt(12) (qmax Delta_max <= 1.5) in
+    each of d channels times codes of rms 3.3, over sqrt(d): 4e-7 rms; exp2 and the rounding of F S - m less than that.  The
+    sums of a warp and of the partials are fp32, their rounding 2^-24 times the root of some hundred steps: 6e-7.  Bound: 2^-18,
+    five times their sum in squares."""
+    ks, vs = make_store(n, 1, d, n, spread=0.0), make_store(n, 1, d, n + 1, spread=0.0)
+    q = queries((1, G, d), n % 97)
+    ref, _, _, _ = reference(ks, vs, q, n)
+    out = F.store_attend(ks, vs, q).double().cpu().numpy()
+    assert np.linalg.norm(out - ref) <= 2.0 ** -18 * np.linalg.norm(ref)
+    assert abs((out - ref).mean()) <= 2.0 ** -18 * np.abs(ref).mean()
