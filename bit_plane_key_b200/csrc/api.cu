@@ -479,7 +479,8 @@ int resolve_rows(const uint16_t* rows, int64_t row_stride, int d, int host, cons
     return FATHOM_OK;
 }
 inline bool dtype_ok(int t) { return t == FATHOM_F32 || t == FATHOM_BF16; }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool aligned(const void* p, unsigned to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+inline bool aligned16(const void* p) { return aligned(p, 16); }
 }  // namespace
 
 int fathom_qk_norm_rope(const void* qkv, int dtype, int64_t token_stride, int n_tokens, int n_q_heads, int n_kv_heads,
@@ -497,7 +498,9 @@ int fathom_qk_norm_rope(const void* qkv, int dtype, int64_t token_stride, int n_
     if (token_stride < (int64_t)(n_q_heads + 2 * n_kv_heads) * d || token_stride % per16) return FATHOM_EINVAL;
     if (row0 < 0 || rows_n < n_tokens || row0 > rows_n - n_tokens || (!positions && row0 + n_tokens - 1 > INT32_MAX))
         return FATHOM_EINVAL;
-    if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(q_weight) || !aligned16(k_weight)) return FATHOM_EINVAL;
+    if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(q_weight) || !aligned16(k_weight) ||
+        !aligned(positions, 4) || !aligned(inv_freq, 4))
+        return FATHOM_EINVAL;
     const uint16_t *kr, *vr;
     int rc = resolve_rows(K_rows, row_stride, d, rows_host_resident, &kr);
     if (!rc) rc = resolve_rows(V_rows, row_stride, d, rows_host_resident, &vr);
@@ -555,7 +558,8 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
     rc = resolve_rows(K_rows, row_stride, K->d, rows_host_resident, &kr);
     if (rc) return rc;
     if (V) {
-        if (V->n != K->n || V->n_kv_heads != K->n_kv_heads || V->d != K->d || V->planes == K->planes)
+        if (V->n != K->n || V->n_kv_heads != K->n_kv_heads || V->d != K->d || V->planes == K->planes ||
+            V->scales == K->scales)
             return FATHOM_EINVAL;
         rc = resolve_growing(V, n_new, dev, &vp, &vsc);
         if (!rc) rc = resolve_rows(V_rows, row_stride, K->d, rows_host_resident, &vr);
@@ -587,7 +591,7 @@ int store_attend(const fathom_store* Ks, const fathom_store* Vs, int S, const vo
     float* dst = parts ? parts : out;
     if (!Ks || !Vs || S < 1 || S > kMaxSets || !q || !dst || !ws || T < 1 || T > kMaxAttendTokens)
         return FATHOM_EINVAL;
-    if (!dtype_ok(q_dtype) || Hq > 65536) return FATHOM_EINVAL;
+    if (!dtype_ok(q_dtype) || Hq > 65536 || !aligned(q, q_dtype == FATHOM_F32 ? 4 : 2) || !aligned(dst, 4)) return FATHOM_EINVAL;
     const int Hkv = Ks[0].n_kv_heads, d = Ks[0].d;
     if (!dims_ok(Hkv, d) || !heads_ok(Hq, Hkv)) return FATHOM_EINVAL;
     if (d != 32 && d != 64 && d != 128 && d != 256) return FATHOM_EUNSUPPORTED;
@@ -601,7 +605,7 @@ int store_attend(const fathom_store* Ks, const fathom_store* Vs, int S, const vo
         AttendMap& m = maps[s / kAttendSets];
         const int e = s % kAttendSets;
         const fathom_store &k = Ks[s], &v = Vs[s];
-        if (k.n_kv_heads != Hkv || v.n_kv_heads != Hkv || k.d != d || v.d != d || k.n != v.n || k.n > INT32_MAX)
+        if (k.n_kv_heads != Hkv || v.n_kv_heads != Hkv || k.d != d || v.d != d || k.n != v.n || k.n > kMaxAttendKeys)
             return FATHOM_EINVAL;
         // an empty store needs no arrays' contents, but is checked like any other
         int rc = resolve_growing(&k, k.n > 0 ? k.n : 1, dev, &m.k_planes[e], &m.k_scales[e]);

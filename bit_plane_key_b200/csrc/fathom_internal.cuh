@@ -15,6 +15,7 @@ constexpr int kPad = 1024;     // key padding granule of the store: plane rows s
 constexpr int kMaxD = 256;     // largest supported head dimension
 constexpr int kMaxTopK = 4096; // largest supported k
 constexpr int kMaxAttendTokens = 4096; // largest query token count of an attention over stores
+constexpr int64_t kMaxAttendKeys = INT32_MAX - 2 * kMaxAttendTokens;   // keys + tokens + a tile fit 32 bits
 constexpr size_t kMaxSmem = 227 * 1024;  // opt-in shared memory per CTA on sm_100
 
 __host__ __device__ inline int64_t n_pad_of(int64_t n) { return ((n + kPad - 1) / kPad) * kPad; }

@@ -21,7 +21,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 OK, EINVAL, ENOMEM, ECUDA, ETIMEOUT, EUNSUPPORTED = range(6)
 F32, BF16 = 0, 1
-DEV_BAD_DEPTH, DEV_BAD_INDEX, DEV_TOPK_OVERFLOW = 1, 2, 4
+DEV_BAD_DEPTH, DEV_BAD_INDEX, DEV_TOPK_OVERFLOW, DEV_TIMEOUT = 1, 2, 4, 8
 MAX_TOPK = 4096
 
 
@@ -473,7 +473,7 @@ def qk_norm_rope(qkv, n_q_heads, n_kv_heads, inv_freq, K_rows, V_rows, row0, q_w
     if positions is not None:
         _check_is(positions, (T,), torch.int32, "positions")
     if out is None:
-        out = qkv.new_empty((T, n_q_heads, d))
+        out = _empty(qkv, (T, n_q_heads, d), qkv.dtype, stream)
     else:
         _check_is(out, (T, n_q_heads, d), qkv.dtype, "out")
     if T == 0:
@@ -510,20 +510,28 @@ def store_attend_workspace_bytes(store, n_sessions, n_tokens, n_q_heads):
                                                         store.n_kv_heads, store.d))
 
 
-def _attend_args(store, q, lead, out, width, workspace):
+def _empty(like, shape, dtype, stream):
+    """New memory that belongs to the stream of the call: once freed, it is used again behind the call alone."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _attend_args(store, q, lead, out, width, workspace, stream):
     """Checks q [lead...][Hq][d] and makes out f32 [lead...][Hq][width] and the workspace."""
     shape = q.shape
     if len(shape) != lead + 2 or lead < 0 or shape[-1] != store.d or not q.is_contiguous():
         raise ValueError("q must be contiguous [...][Hq][d] with d = %d" % store.d)
     want = shape if width == store.d else shape[:-1] + (width,)
     if out is None:
-        out = q.new_empty(want, dtype=torch.float32)
+        out = _empty(q, want, torch.float32, stream)
     else:
         _check_is(out, want, torch.float32, "out")
     T = shape[-3] if lead else 1
     if workspace is None:
         nb = store_attend_workspace_bytes(store, shape[0] if lead == 2 else 1, T, shape[-2])
-        workspace = q.new_empty(max(nb, 1), dtype=torch.uint8)
+        workspace = _empty(q, (max(nb, 1),), torch.uint8, stream)
     return out, T, workspace
 
 
@@ -538,7 +546,7 @@ def store_attend(k_store, v_store, q, causal=True, out=None, workspace=None, str
     store: q [Hq][d] or [T][Hq][d] -> f32 of the same shape.  causal: the stores'
     last T keys are the T tokens' own, each sees its past and itself; else every
     token sees all keys."""
-    out, T, workspace = _attend_args(k_store, q, _attend_lead(q), out, k_store.d, workspace)
+    out, T, workspace = _attend_args(k_store, q, _attend_lead(q), out, k_store.d, workspace, stream)
     _check(_lib.fathom_store_attend(k_store.c, v_store.c, _ptr(q), _dtype_code(q), T, q.shape[-2], int(bool(causal)),
                                     _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
            "fathom_store_attend")
@@ -548,7 +556,7 @@ def store_attend(k_store, v_store, q, causal=True, out=None, workspace=None, str
 def store_attend_partial(k_store, v_store, q, visible, parts=None, workspace=None, stream=None):
     """Partials f32 [..][Hq][d + 2] (as sparse_attend_partial) of attention over
     this range's keys; token t sees those below visible + t."""
-    parts, T, workspace = _attend_args(k_store, q, _attend_lead(q), parts, k_store.d + 2, workspace)
+    parts, T, workspace = _attend_args(k_store, q, _attend_lead(q), parts, k_store.d + 2, workspace, stream)
     _check(_lib.fathom_store_attend_partial(k_store.c, v_store.c, _ptr(q), _dtype_code(q), T, q.shape[-2],
                                             int(visible), _ptr(parts), _ptr(workspace), workspace.numel(),
                                             _stream(stream)), "fathom_store_attend_partial")
@@ -558,9 +566,9 @@ def store_attend_partial(k_store, v_store, q, visible, parts=None, workspace=Non
 def store_attend_batched(k_stores, v_stores, q, causal=True, out=None, workspace=None, stream=None):
     """store_attend of the sessions (k_stores[s], v_stores[s]) in one pass: q
     [S][T][Hq][d] -> f32 of the same shape."""
-    if len(k_stores) != q.shape[0] or len(v_stores) != q.shape[0]:
+    if not k_stores or len(k_stores) != q.shape[0] or len(v_stores) != q.shape[0]:
         raise ValueError("one K store and one V store for each session of q")
-    out, T, workspace = _attend_args(k_stores[0], q, 2, out, k_stores[0].d, workspace)
+    out, T, workspace = _attend_args(k_stores[0], q, 2, out, k_stores[0].d, workspace, stream)
     _check(_lib.fathom_store_attend_batched(_store_array(k_stores), _store_array(v_stores), len(k_stores), _ptr(q),
                                             _dtype_code(q), T, q.shape[-2], int(bool(causal)), _ptr(out),
                                             _ptr(workspace), workspace.numel(), _stream(stream)),

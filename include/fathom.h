@@ -453,7 +453,7 @@ int fathom_qk_norm_rope(const void* qkv, int dtype, int64_t token_stride, int n_
  * The result equals fathom_append_keys of the same rows, bit for bit.  Rows hold
  * finite values.
  * Errors: EINVAL for null pointers, n_new <= n, missing capacity, stores that
- * differ or share planes, arrays not where the flags say or misaligned.
+ * differ or share planes or scales, arrays not where the flags say or misaligned.
  */
 int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows, const uint16_t* V_rows,
                        int64_t row_stride, int rows_host_resident, int64_t rows_n, int64_t n_new,
@@ -469,16 +469,18 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
  *   fp32 accumulation; 0 for a token that sees no key.
  * causal != 0: the stores' last n_tokens keys are the tokens' own, token t sees
  * the keys below n - n_tokens + 1 + t.  causal == 0: every token sees all n keys.
- *   K, V      stores with the same n, Hkv, d, n <= 2^31 - 1; each device- or
+ *   K, V      stores with the same n, Hkv, d, n < 2^31 - 8192; each device- or
  *             host-resident; n may be 0.
- *   q         device, [n_tokens][Hq][d], FATHOM_F32 or FATHOM_BF16, finite values;
- *             1 <= n_tokens <= 4096 (made for few tokens: the stores are read again
- *             for every 8 (token, head of a group) pairs).
+ *   q         device, [n_tokens][Hq][d], FATHOM_F32 or FATHOM_BF16, finite values, the
+ *             largest times the largest scale below 2^112; 1 <= n_tokens <= 4096 (made
+ *             for few tokens: the stores are read again for every 8 (token, head of a
+ *             group) pairs).
  *   out       device, f32 [n_tokens][Hq][d].
  *   workspace device, 256-byte aligned, fathom_store_attend_workspace_bytes() bytes;
  *             contents need not be initialised, and are free once the call's
  *             kernels are done.  Calls that overlap on the GPU need one each.
- * A call with the same arguments gives the same bits.  The call's kernels are
+ * A call with the same arguments gives the same bits.  A captured call keeps the n
+ * that the stores had when it was captured.  The call's kernels are
  * launched with programmatic serialization: they are scheduled while the kernel
  * before them in the stream finishes, and wait for it before they read or write.
  * Errors: EINVAL for null pointers, bad sizes, stores that differ, arrays not on
@@ -497,7 +499,8 @@ int fathom_store_attend(const fathom_store* K, const fathom_store* V, const void
  *   visible   token t sees the keys of this range below visible + t (any value:
  *             negative or 0 for a range behind the tokens, >= n for all keys).
  *   parts     device, f32 [n_tokens][Hq][d + 2], as fathom_sparse_attend_partial
- *             writes them; the two kinds may be merged with each other.
+ *             writes them; the two kinds may be merged with each other.  m is a whole number,
+ *             above the largest score (in log2 units) by less than 1.
  */
 int fathom_store_attend_partial(const fathom_store* K, const fathom_store* V, const void* q, int q_dtype, int n_tokens,
                                 int n_q_heads, int64_t visible, float* parts, void* workspace, size_t workspace_bytes,

@@ -1,15 +1,23 @@
 """Attention over the 4-bit stores (fathom_store_attend, _partial, _batched)
 against the definition in 64 bits.
 
-Tolerance.  The logits are sums over d channels of q Delta code, offsets
-included, so their rounding is relative to A = 15 sum_c |q_c| Delta_c / sqrt(d)
-of the block.  Sixteen channels enter per accumulation step with at most two
-units of the last place of the partial sum (2^-23 A), the split of q Delta into
-two halves of 11 bits adds 2^-22, the scaling of the result 2 roundings: a logit
-is off by at most e = (d/16 + 6) 2^-23 A, and the largest A of any visible
-block serves for all.  The weights then move by a factor of at most e^(2e), and
-exp2 and the sums over keys add at most 2^-22 per step over (n/64 + 64) steps.
-Both act on sum_i p_i 15 Delta_i,c.
+Tolerance, as the sum of
+- logits.  Sums over d channels of q Delta code, offsets included, so their
+  rounding is relative to A = 15 sum_c |q_c| Delta_c / sqrt(d) of the block.  Sixteen
+  channels enter per accumulation step with at most two units of the last place of
+  the partial sum (2^-23 A), the split of q Delta into two halves leaves 2^-22, the
+  scaling of the result 2 roundings: (d/16 + 6) 2^-23 A; and each channel's low half at
+  least a rounding of 2^-25 of max |q| max Delta, so 15 sqrt(d) 2^-25 times that more.
+  A logit is off by at most e, the sum of both; the largest A and Delta of any
+  visible block serve for all.  The weights move by a factor of at most exp(2e).
+- weights.  exp2 is off by 2^-22; its argument, below 64 in magnitude where the weight
+  counts, is rounded by 2^-19; in numerator and sum: 2^-17 with room.  A weight's low half is
+  rounded to 2^-23 of the largest weight in its block of 64 keys, or, as a fp16
+  subnormal, to 2^-36 of the largest of all.
+- sums over keys.  A warp adds two blocks a tile, then 8 warps and the partials are
+  added: at most n/512 + 24 steps of two roundings (2^-24) and one rescaling (2^-22), in
+  numerator and sum.
+All act on sum_i p_i 15 Delta_i,c, the last but one on its own weights.
 """
 import math
 
@@ -78,7 +86,11 @@ def reference(ks, vs, q, visible):
             out[t, h] = p @ V[g, :see]
             A = 15 * (Kd[g, :see] @ np.abs(q[t, h])).max() / math.sqrt(d)
             e = (d / 16 + 6) * 2.0 ** -23 * A
-            tol[t, h] = (np.expm1(2 * e) + (n / 64 + 64) * 2.0 ** -22) * 15 * (p @ Vd[g, :see])
+            e += 15 * math.sqrt(d) * 2.0 ** -25 * np.abs(q[t, h]).max() * Kd[g, :see].max()
+            pV = p @ Vd[g, :see]
+            tol[t, h] = (np.expm1(2 * e) + 2.0 ** -17 + 1.5 * (n / 512 + 24) * 2.0 ** -22) * 15 * pV
+            top = np.repeat([p[i:i + 64].max() for i in range(0, see, 64)], 64)[:see] * 2.0 ** -23 + 2.0 ** -35 * p.max()
+            tol[t, h] += 15 * (top @ Vd[g, :see]) + 7.5 * top.sum() * pV
     return out, tol, M, L
 
 
@@ -428,6 +440,36 @@ def test_back_to_back_calls_in_one_workspace():
         for g, (_, _, _, want) in zip(got, items):
             assert torch.equal(g, want)
     assert F.last_device_status() == 0
+
+
+
+def test_calls_on_a_stream_of_their_own_leave_their_memory_to_it():
+    """Temporaries of calls on another stream are not handed to the current stream while those calls run."""
+    ks, vs = make_store(60000, 1, 64, 1), make_store(60000, 1, 64, 2)
+    q = queries((4, 64), 3)
+    want = F.store_attend(ks, vs, q)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    nb = F.store_attend_workspace_bytes(ks, 1, 1, 4)
+    got = []
+    for _ in range(20):
+        got.append(F.store_attend(ks, vs, q, stream=side))
+        torch.empty(nb, dtype=torch.uint8, device=DEV).fill_(255)     # would be the workspace of the call before
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
+def test_misaligned_pointers_and_empty_batches_are_refused():
+    ks, vs = make_store(100, 2, 64, 1), make_store(100, 2, 64, 2)
+    ws = torch.empty(F.store_attend_workspace_bytes(ks, 1, 1, 8), dtype=torch.uint8, device=DEV)
+    buf, out = torch.zeros(8 * 64 * 4 + 16, dtype=torch.uint8, device=DEV), torch.zeros(8 * 64 + 4, device=DEV)
+    L, p, o = F.lib(), buf.data_ptr(), out.data_ptr()
+    for at, dt, dst in ((p + 2, F.F32, o), (p + 1, F.BF16, o), (p, F.BF16, o + 2)):
+        assert L.fathom_store_attend(ks.c, vs.c, at, dt, 1, 8, 1, dst, ws.data_ptr(), ws.numel(), None) == F.EINVAL
+    assert L.fathom_store_attend(ks.c, vs.c, p + 2, F.BF16, 1, 8, 1, o + 4, ws.data_ptr(), ws.numel(), None) == F.OK
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError):
+        F.store_attend_batched([], [], torch.zeros(0, 1, 8, 64, device=DEV))
 
 
 @pytest.mark.parametrize("n,d,G", [(131072, 64, 4), (60000, 128, 8), (4000, 256, 2)])

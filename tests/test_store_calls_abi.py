@@ -27,7 +27,8 @@ def test_row_and_store_attention_calls_reject_bad_arguments(libpath):
                 dict(wq=fake), dict(wk=fake), dict(wq=fake, wk=fake, wdt=5), dict(eps=-1.0), dict(eps=float("nan")),
                 dict(inv=None), dict(rot=72), dict(rot=80), dict(rot=-16), dict(rows=2), dict(row0=8), dict(row0=-1),
                 dict(row0=1 << 62, rows=1 << 62), dict(rows=1 << 40, row0=(1 << 31)), dict(qkv=ctypes.c_void_p(8 + 4096)),
-                dict(rs=60), dict(rs=68), dict(K=ctypes.c_void_p(4096 + 2))):
+                dict(rs=60), dict(rs=68), dict(K=ctypes.c_void_p(4096 + 2)), dict(pos=ctypes.c_void_p(4096 + 2)),
+                dict(inv=ctypes.c_void_p(4096 + 1))):
         assert rope(**bad) == F.EINVAL, bad
 
     def store(n=100, n_pad=1024, Hkv=2, d=64, host=0, planes=1 << 12, scales=1 << 13):
