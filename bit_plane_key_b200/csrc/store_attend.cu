@@ -6,29 +6,47 @@
 //
 // over the keys a query may see, in one pass with a running maximum and sum.
 //
-// Work split.  The keys of a (session, KV head, set of queries) are a row of
-// tiles of kTile keys.  All rows' tiles form one list, cut into equal runs,
-// one per CTA; a run may end in the middle of a row, so every (CTA, row) pair
+// Work split.  The keys of a (session, KV head, set of 4 or 8 (token, head of the
+// group) pairs) are a row of tiles of 1024 keys (512 where a call is short).  All
+// rows' tiles form one list, cut into equal runs, one per CTA, at most as many as
+// are resident; a run may end in the middle of a row, so every (CTA, row) pair
 // leaves a partial (o, m, l), and a second launch adds a row's partials in
 // order.  CTA p's partial of row r lies in slot p + r: a run that passes into
 // the next row raises r, a row that passes into the next CTA raises p, so no
 // two meet.
 //
-// A tile.  The CTA's warps turn the plane words of 8 blocks of 64 keys into
-// words of 4-bit codes in shared memory, laid out so that one 16-byte load is
-// a lane's share of a matrix operand; then each warp takes one block through
-// both products, m16n8k16 on fp16 with fp32 sums:
+// A tile.  Its planes arrive in chunks of 32 channels, K's then V's, by one
+// tensor copy each into a ring of four buffers: 128 bytes of every plane row, a
+// whole line (pieces of 64 bytes end at 3 TB/s, of 32 at 1.6).  Eight warps have
+// two blocks of 64 keys each, and no step of theirs waits for another warp
+// but the copy that reuses a buffer, which they issue in turn.  A warp turns the
+// plane words of its blocks into words of 4-bit codes in its own shared memory,
+// laid out so that one 16-byte load is a lane's share of a matrix operand, and
+// takes them through both products, m16n8k16 on fp16 with fp32 sums:
 //   S (64 keys x columns) = codes . Q',  Q'_c = q_c Delta_c of this block,
 //   O (d x columns) += Delta_c (codes . P).
 // A code needs no conversion: the bits 0..15 of an fp16 are the subnormal
 // code 2^-24, exactly, and shifted by 4 bits 16 times that, so one AND makes
-// two operand values; the factors are undone in the scaling of S and P, and
-// the offset 7.5 by one more product with a constant 15.
-// Q' and P are split into two fp16 halves of 11 bits each, which sit in
-// neighbouring columns, so that a column pair of the 8 is one query in 22
-// bits: the products lose no more than fp32 arithmetic would.  Scores never
-// leave the warp: a transposing move of 8x8 matrices makes the P operand of
-// the S accumulators.
+// two operand values; the factors are undone in the scaling of S and P.  The
+// offset 7.5 is half of one more product, with a constant 15.
+// Scores never leave the warp: a transposing move of 8x8 matrices makes the P
+// operand of the S accumulators.
+//
+// Precision.  Q' and P are split into a high and a low fp16 half, which sit in
+// neighbouring columns, so that a column pair of the 8 is one query in some 22
+// bits.  The matrix unit cuts every addend off at 2^-23 of the largest, always
+// toward zero: with codes that are all positive, sums over n keys drift
+// from the true one, by 1e-4 of the output at 131072 keys.  So the high halves are
+// multiples of a power of two that is large enough for their sums to be exact, as
+// the offset is; what is cut off the low halves' sums is 2^-10 smaller.  The running
+// maximum is rounded up to a whole number of binary orders: what was summed
+// is rescaled exactly.  Against 64 bits: 2e-7 to 7e-7 of the output (fp32 arithmetic: 2e-7
+// to 2.6e-6).
+//
+// What bounds it: the instructions around the products, ALU and issue slots, not the
+// memory: 0.29 us per 64-key block and SM where the copies alone take 0.20; and
+// 13 us of launches, first copies and merge.  1048576 keys (4 heads of 128, 4 queries
+// each): 272 us, 4.2 TB/s; 131072: 47 us; 4096 keys of 1 head: 8.8 us.
 #include <cuda.h>
 
 #include "fathom_internal.cuh"
@@ -125,7 +143,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// loads that stay where they are written: ahead of the work that hides them
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 // (low, high) as two fp16
 __device__ __forceinline__ uint32_t half2_of(float low, float high) {
@@ -134,11 +151,10 @@ __device__ __forceinline__ uint32_t half2_of(float low, float high) {
     return r;
 }
 // Two values v = q Delta below 2^14, q = q1 + q2, as a column's operand.  Even column:
-// the high half h, v's whole number in 10 bits or more (the sum with 1536 of an fp16
-// up to 2^14 has no fraction).  Odd column: q1 Delta - h, rounded once, + q2 Delta.
-// Sums of the high halves' products with codes are whole numbers, too: the matrix
-// unit, which cuts addends off where fp32 would round a sum, adds them exactly
-// below 2^24, as it would not products of an fp16's full range.
+// the high half h, v to a multiple of 1/2 or more (the sum with 1536 of an fp16 below
+// 2^14 has no finer bits).  Odd column: q1 Delta - h, rounded once, + q2 Delta, of at
+// most 2^-11 of v or 1/2.  Sums of the high halves' products with codes are multiples
+// of 1/2, too, and exact up to 2^23 of them.
 __device__ __forceinline__ uint32_t half_of_product(uint32_t q1, uint32_t own, uint32_t q2, uint32_t delta, __half2 sign, bool f32) {
     const __half2 d = as_half2(delta), big = __float2half2_rn(1536.0f);
     const __half2 h = __hadd2_rn(__hfma2(as_half2(q1), d, big), __hneg2(big));
@@ -155,7 +171,9 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y, uint32_t mask) 
 }
 
 // The ring of raw planes: a chunk's bytes arrive by one asynchronous tensor
-// copy.  A wait gives up after 2^22 tries (seconds), which no correct run reaches.
+// copy.  A wait gives up after 2^31 clocks, about a second, which no correct run
+// reaches; that warp then waits no more, issues no further copy, leaves time for
+// those in flight, and reports.
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void barrier_init(uint64_t* b, int count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count) : "memory");
@@ -170,7 +188,8 @@ __device__ __forceinline__ bool barrier_try(uint64_t* b, uint32_t parity) {
 }
 __device__ __forceinline__ bool barrier_wait(uint64_t* b, uint32_t parity) {
     if (barrier_try(b, parity)) return true;
-    for (int i = 0; i < (1 << 22); ++i)
+    const uint32_t start = (uint32_t)clock();
+    while ((uint32_t)clock() - start < 1u << 31)
         if (barrier_try(b, parity)) return true;
     return false;
 }
@@ -270,7 +289,8 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
     uint32_t* s_raw = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u) / 4;   // the next 1024-byte boundary
     // [ring][plane][channel][row of the tile], 16-byte pieces swizzled by the channel
     uint32_t* s_codes = s_raw + kRing * Sh::kRaw;       // [warp][block][ks][lane][4] code words
-    uint16_t* s_rs = reinterpret_cast<uint16_t*>(s_codes + kWarps * Sh::kOwn);     // [K, V][D][blocks of the tile] scales, the 16-byte pieces of 32 swizzled by the channel's bit 2
+    // [K, V][D][blocks of the tile] scales, the 16-byte pieces of 32 swizzled by the channel's bit 2
+    uint16_t* s_rs = reinterpret_cast<uint16_t*>(s_codes + kWarps * Sh::kOwn);
     uint16_t* s_sc = s_rs + 2 * Sh::kRawScales;         // [warp][K, V][block][D] scales, K's times the block's factor
     uint32_t* s_q = reinterpret_cast<uint32_t*>(s_sc + kWarps * Sh::kScales);      // [NT][ks][lane][4]
     uint32_t* s_q2 = s_q + Sh::kQWords;                 // [NT][ks][lane][2], f32 queries only
@@ -392,7 +412,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
             {
                 const uint32_t keep = act ? (NB == 2 && k0 + kBlock < most ? 0xFFFFFFFFu : 0xFFFFu) : 0u;
                 __half2 mh = __float2half2_rn(0.0f);
-                stuck |= !barrier_wait(s_full + kRing, u & 1);
+                stuck = stuck || !barrier_wait(s_full + kRing, u & 1);
                 uint32_t sw[2 * D / 32];                // of the warp's blocks: K's channels, then V's
 #pragma unroll
                 for (int i = 0; i < 2 * D / 32; ++i) {
@@ -451,7 +471,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
             auto stage = [&](bool isk, int c) {
                 const int rj = (2 * NC) % kRing == 0 ? c % kRing : j % kRing;
                 const uint32_t turn = (uint32_t)((2 * NC) % (2 * kRing) == 0 ? c / kRing : j / kRing) & 1;
-                stuck |= !barrier_wait(s_full + rj, turn);
+                stuck = stuck || !barrier_wait(s_full + rj, turn);
                 // pieces of 16 bytes: a warp's two blocks of 128 keys, or the two warps' of 64 that share one
                 const uint32_t* src = s_raw + rj * Sh::kRaw + pl * Sh::kRow;
                 const int piece = NB == 2 ? wp : wp / 2, swizzle = NB == 2 ? pl & 7 : (pl >> 1) & 3;
@@ -515,16 +535,16 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 }
                 // warps take turns at the copy of the buffer's next chunk, once every warp has read this one
                 if (wp == ((2 * NC) % kWarps == 0 ? c : j) % kWarps && j + kRing < chunks) {
-                    stuck |= !barrier_wait(s_read + rj, turn);
+                    stuck = stuck || !barrier_wait(s_read + rj, turn);
                     const int cn = c + kRing, un = u + cn / (2 * NC);
-                    if (lane == 0) {
+                    if (lane == 0 && !stuck) {
                         if (un < re) copy(rw, ub + un, cn % (2 * NC), rj);
                         else copy(row_of(map.at, ub + un, Hkv, sets), ub + un, cn % (2 * NC), rj);
                     }
                 }
                 if (c == 1 && wp == u % kWarps && u + 1 < units) {   // and at that of the next tile's scales
-                    stuck |= !barrier_wait(s_read + kRing, u & 1);
-                    if (lane == 0) copy_scale(u + 1 < re ? rw : row_of(map.at, ub + u + 1, Hkv, sets), ub + u + 1);
+                    stuck = stuck || !barrier_wait(s_read + kRing, u & 1);
+                    if (lane == 0 && !stuck) copy_scale(u + 1 < re ? rw : row_of(map.at, ub + u + 1, Hkv, sets), ub + u + 1);
                 }
                 ++j;
                 __syncwarp();
@@ -567,100 +587,100 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 }
             }
             if (act) {
-                    // ---- weights: lane (g, t) holds query t of the tile, 8 keys of each block
-                    const bool cut = k0 + NB * kBlock > least;   // some query of the set does not see all keys
-                    float shift[NT];
-                    bool moved = false;
+                // ---- weights: lane (g, t) holds query t of the tile, 8 keys of each block
+                const bool cut = k0 + NB * kBlock > least;   // some query of the set does not see all keys
+                float shift[NT];
+                bool moved = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float f = s_f[nt * kTilePairs + lt];
+                    float F[NB], top[NB];
+                    float mn = m[nt];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const float un = (p & 1) ? 0.0625f : 1.0f;
+                            float* v = S[b][nt][p];
+                            // the high halves' sums, and their offset, are exact
+                            v[0] = fmaf(v[0], un, -0.5f * B15[b][nt][0]) + fmaf(v[1], un, -0.5f * B15[b][nt][1]);
+                            v[2] = fmaf(v[2], un, -0.5f * B15[b][nt][0]) + fmaf(v[3], un, -0.5f * B15[b][nt][1]);
+                            if (cut) {
+                                const int key = k0 + b * kBlock + 4 * (p + 4 * (lg & 1)) + (lg >> 1);
+                                if (key >= limit[nt]) v[0] = -INFINITY;
+                                if (key + 32 >= limit[nt]) v[2] = -INFINITY;
+                            }
+                            mx = fmaxf(mx, fmaxf(v[0], v[2]));
+                        }
+                        F[b] = f * back[b];
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        top[b] = mx * F[b];
+                        // a whole number: what was summed so far is rescaled by powers of two, exactly
+                        mn = fmaxf(mn, ceilf(top[b]));
+                    }
+                    const float base = mn == -INFINITY ? 0.0f : mn;
+                    // S F - base is rounded once; where the product's own rounding exceeds
+                    // the exponents that matter, both are rounded alike instead
+                    if (fabsf(base) > 1048576.0f) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                S[b][nt][p][0] *= F[b];
+                                S[b][nt][p][2] *= F[b];
+                            }
+                            F[b] = 1.0f;
+                        }
+                    }
+                    shift[nt] = ex2(m[nt] - base);      // 0 while nothing has been seen
+                    moved |= mn != m[nt];
+                    m[nt] = mn;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        // the high halves of a block's weights are multiples of 2^-11 of (the power of two above)
+                        // the largest: P + round is rounded to one
+                        const float round = __uint_as_float(__float_as_uint(ex2(top[b] - base)) & 0x7F800000u) * 0x1.8p28f;
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            // weights times 2^15, or 2^11 where the codes come 16 times as large
+                            const float up = (p & 1) ? 2048.0f : 32768.0f, r = (p & 1) ? round * 0.0625f : round;
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) {
+                                const float v = ex2(fmaf(S[b][nt][p][2 * w], F[b], -base)) * up;
+                                const float h = __fadd_rn(__fadd_rn(v, r), -r);
+                                S[b][nt][p][w] = __uint_as_float(transpose8x8(half2_of(h, v - h)));
+                            }
+                        }
+                    }
+                }
+                if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float f = s_f[nt * kTilePairs + lt];
-                        float F[NB], top[NB];
-                        float mn = m[nt];
+                        l[nt] *= shift[nt];
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            float mx = -INFINITY;
-#pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                const float un = (p & 1) ? 0.0625f : 1.0f;
-                                float* v = S[b][nt][p];
-                                // the high halves' sums, and their offset, are exact
-                                v[0] = fmaf(v[0], un, -0.5f * B15[b][nt][0]) + fmaf(v[1], un, -0.5f * B15[b][nt][1]);
-                                v[2] = fmaf(v[2], un, -0.5f * B15[b][nt][0]) + fmaf(v[3], un, -0.5f * B15[b][nt][1]);
-                                if (cut) {
-                                    const int key = k0 + b * kBlock + 4 * (p + 4 * (lg & 1)) + (lg >> 1);
-                                    if (key >= limit[nt]) v[0] = -INFINITY;
-                                    if (key + 32 >= limit[nt]) v[2] = -INFINITY;
-                                }
-                                mx = fmaxf(mx, fmaxf(v[0], v[2]));
-                            }
-                            F[b] = f * back[b];
-#pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            top[b] = mx * F[b];
-                            // a whole number: what was summed so far is rescaled by powers of two, exactly
-                            mn = fmaxf(mn, ceilf(top[b]));
-                        }
-                        const float base = mn == -INFINITY ? 0.0f : mn;
-                        // S F - base is rounded once; where the product's own rounding exceeds
-                        // the exponents that matter, both are rounded alike instead
-                        if (fabsf(base) > 1048576.0f) {
-#pragma unroll
-                            for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                                for (int p = 0; p < 4; ++p) {
-                                    S[b][nt][p][0] *= F[b];
-                                    S[b][nt][p][2] *= F[b];
-                                }
-                                F[b] = 1.0f;
-                            }
-                        }
-                        shift[nt] = ex2(m[nt] - base);      // 0 while nothing has been seen
-                        moved |= mn != m[nt];
-                        m[nt] = mn;
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            // the high halves of a block's weights are multiples of 2^-11 of (the power of two above)
-                            // the largest: P + round is rounded to one
-                            const float round = __uint_as_float(__float_as_uint(ex2(top[b] - base)) & 0x7F800000u) * 0x1.8p28f;
-#pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                // weights times 2^15, or 2^11 where the codes come 16 times as large
-                                const float up = (p & 1) ? 2048.0f : 32768.0f, r = (p & 1) ? round * 0.0625f : round;
-#pragma unroll
-                                for (int w = 0; w < 2; ++w) {
-                                    const float v = ex2(fmaf(S[b][nt][p][2 * w], F[b], -base)) * up;
-                                    const float h = __fadd_rn(__fadd_rn(v, r), -r);
-                                    S[b][nt][p][w] = __uint_as_float(transpose8x8(half2_of(h, v - h)));
-                                }
-                            }
+                        for (int mt = 0; mt < KS; ++mt) {
+                            O[nt][mt][0] *= shift[nt];
+                            O[nt][mt][1] *= shift[nt];
                         }
                     }
-                    if (__any_sync(0xffffffffu, moved)) {
+                }
+                // ---- 15 sum P: the offset of the codes, and the weights' sum
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            l[nt] *= shift[nt];
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int mt = 0; mt < KS; ++mt) {
-                                O[nt][mt][0] *= shift[nt];
-                                O[nt][mt][1] *= shift[nt];
-                            }
+                    for (int b = 0; b < NB; ++b) {
+                        float c4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const uint32_t v15 = (p & 1) ? 0x00F000F0u : 0x000F000Fu, a[4] = {v15, v15, v15, v15};
+                            mma_p(c4, a, S[b][nt][p]);
                         }
+                        neg[b][nt][0] = -0.5f * c4[0];
+                        neg[b][nt][1] = -0.5f * c4[1];
+                        l[nt] = fmaf(c4[0] + c4[1], 512.0f / 15.0f, l[nt]);   // 2^24 / 2^15
                     }
-                    // ---- 15 sum P: the offset of the codes, and the weights' sum
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            float c4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                const uint32_t v15 = (p & 1) ? 0x00F000F0u : 0x000F000Fu, a[4] = {v15, v15, v15, v15};
-                                mma_p(c4, a, S[b][nt][p]);
-                            }
-                            neg[b][nt][0] = -0.5f * c4[0];
-                            neg[b][nt][1] = -0.5f * c4[1];
-                            l[nt] = fmaf(c4[0] + c4[1], 512.0f / 15.0f, l[nt]);   // 2^24 / 2^15
-                        }
             }
 #pragma unroll
             for (int cv = 0; cv < NC; ++cv) {
@@ -669,30 +689,30 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                     // ---- O += Delta (codes - 7.5) . P
                     const uint4* vc = reinterpret_cast<const uint4*>(codes) + (lane ^ ((lane >> 3) & 3));
 #pragma unroll
-                        for (int k = 0; k < CK; ++k) {
-                            const int mt = cv * CK + k;
-                            float acc[NB][NT][4];
+                    for (int k = 0; k < CK; ++k) {
+                        const int mt = cv * CK + k;
+                        float acc[NB][NT][4];
 #pragma unroll
-                            for (int b = 0; b < NB; ++b) {
-                                uint32_t a[4][4];
-                                operands(vc[b * (Sh::kCodes / (4 * NB)) + k * 32], a);
+                        for (int b = 0; b < NB; ++b) {
+                            uint32_t a[4][4];
+                            operands(vc[b * (Sh::kCodes / (4 * NB)) + k * 32], a);
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) acc[b][nt][0] = acc[b][nt][2] = neg[b][nt][0], acc[b][nt][1] = acc[b][nt][3] = neg[b][nt][1];
+                            for (int nt = 0; nt < NT; ++nt) acc[b][nt][0] = acc[b][nt][2] = neg[b][nt][0], acc[b][nt][1] = acc[b][nt][3] = neg[b][nt][1];
 #pragma unroll
-                                for (int p = 0; p < 4; ++p)
+                            for (int p = 0; p < 4; ++p)
 #pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) mma_p(acc[b][nt], a[p], S[b][nt][p]);
-                            }
+                                for (int nt = 0; nt < NT; ++nt) mma_p(acc[b][nt], a[p], S[b][nt][p]);
+                        }
 #pragma unroll
-                            for (int b = 0; b < NB; ++b) {
-                                const float2 dv = __half22float2(*reinterpret_cast<const __half2*>(v_scales + b * D + 16 * mt + 2 * lg));
+                        for (int b = 0; b < NB; ++b) {
+                            const float2 dv = __half22float2(*reinterpret_cast<const __half2*>(v_scales + b * D + 16 * mt + 2 * lg));
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    O[nt][mt][0] = fmaf(acc[b][nt][0] + acc[b][nt][1], dv.x, O[nt][mt][0]);
-                                    O[nt][mt][1] = fmaf(acc[b][nt][2] + acc[b][nt][3], dv.y, O[nt][mt][1]);
-                                }
+                            for (int nt = 0; nt < NT; ++nt) {
+                                O[nt][mt][0] = fmaf(acc[b][nt][0] + acc[b][nt][1], dv.x, O[nt][mt][0]);
+                                O[nt][mt][1] = fmaf(acc[b][nt][2] + acc[b][nt][3], dv.y, O[nt][mt][1]);
                             }
                         }
+                    }
                     __syncwarp();
                 }
             }
@@ -744,7 +764,11 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         __syncthreads();                                // before the next row's queries and codes
         if (u < units) rw = row_of(map.at, ub + u, Hkv, sets);
     }
-    if (stuck && lane == 0) atomicOr(status, (unsigned)FATHOM_DEV_TIMEOUT);
+    if (stuck) {
+        const uint32_t start = (uint32_t)clock();
+        while ((uint32_t)clock() - start < 1u << 31) {}
+        atomicOr(status, (unsigned)FATHOM_DEV_TIMEOUT);
+    }
 }
 
 // One CTA per (row, pair) whose keys were shared by several CTAs, or that has
