@@ -186,12 +186,14 @@ __device__ __forceinline__ bool barrier_try(uint64_t* b, uint32_t parity) {
                  : "memory");
     return done != 0;
 }
-__device__ __forceinline__ bool barrier_wait(uint64_t* b, uint32_t parity) {
-    if (barrier_try(b, parity)) return true;
+__device__ __noinline__ bool barrier_gives_up(uint64_t* b, uint32_t parity) {
     const uint32_t start = (uint32_t)clock();
     while ((uint32_t)clock() - start < 1u << 31)
-        if (barrier_try(b, parity)) return true;
-    return false;
+        if (barrier_try(b, parity)) return false;
+    return true;
+}
+__device__ __forceinline__ void barrier_wait(uint64_t* b, uint32_t parity, bool& stuck) {
+    if (!barrier_try(b, parity) && !stuck) stuck = barrier_gives_up(b, parity);
 }
 // bytes to come before the barrier's phase is over
 __device__ __forceinline__ void barrier_expect(uint64_t* b, uint32_t bytes) {
@@ -412,7 +414,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
             {
                 const uint32_t keep = act ? (NB == 2 && k0 + kBlock < most ? 0xFFFFFFFFu : 0xFFFFu) : 0u;
                 __half2 mh = __float2half2_rn(0.0f);
-                stuck = stuck || !barrier_wait(s_full + kRing, u & 1);
+                barrier_wait(s_full + kRing, u & 1, stuck);
                 uint32_t sw[2 * D / 32];                // of the warp's blocks: K's channels, then V's
 #pragma unroll
                 for (int i = 0; i < 2 * D / 32; ++i) {
@@ -471,7 +473,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
             auto stage = [&](bool isk, int c) {
                 const int rj = (2 * NC) % kRing == 0 ? c % kRing : j % kRing;
                 const uint32_t turn = (uint32_t)((2 * NC) % (2 * kRing) == 0 ? c / kRing : j / kRing) & 1;
-                stuck = stuck || !barrier_wait(s_full + rj, turn);
+                barrier_wait(s_full + rj, turn, stuck);
                 // pieces of 16 bytes: a warp's two blocks of 128 keys, or the two warps' of 64 that share one
                 const uint32_t* src = s_raw + rj * Sh::kRaw + pl * Sh::kRow;
                 const int piece = NB == 2 ? wp : wp / 2, swizzle = NB == 2 ? pl & 7 : (pl >> 1) & 3;
@@ -535,16 +537,12 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 }
                 // warps take turns at the copy of the buffer's next chunk, once every warp has read this one
                 if (wp == ((2 * NC) % kWarps == 0 ? c : j) % kWarps && j + kRing < chunks) {
-                    stuck = stuck || !barrier_wait(s_read + rj, turn);
+                    barrier_wait(s_read + rj, turn, stuck);
                     const int cn = c + kRing, un = u + cn / (2 * NC);
                     if (lane == 0 && !stuck) {
                         if (un < re) copy(rw, ub + un, cn % (2 * NC), rj);
                         else copy(row_of(map.at, ub + un, Hkv, sets), ub + un, cn % (2 * NC), rj);
                     }
-                }
-                if (c == 1 && wp == u % kWarps && u + 1 < units) {   // and at that of the next tile's scales
-                    stuck = stuck || !barrier_wait(s_read + kRing, u & 1);
-                    if (lane == 0 && !stuck) copy_scale(u + 1 < re ? rw : row_of(map.at, ub + u + 1, Hkv, sets), ub + u + 1);
                 }
                 ++j;
                 __syncwarp();
@@ -681,6 +679,11 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                         neg[b][nt][1] = -0.5f * c4[1];
                         l[nt] = fmaf(c4[0] + c4[1], 512.0f / 15.0f, l[nt]);   // 2^24 / 2^15
                     }
+            }
+            // a warp has its turn at the copy of the next tile's scales
+            if (wp == u % kWarps && u + 1 < units) {
+                barrier_wait(s_read + kRing, u & 1, stuck);
+                if (lane == 0 && !stuck) copy_scale(u + 1 < re ? rw : row_of(map.at, ub + u + 1, Hkv, sets), ub + u + 1);
             }
 #pragma unroll
             for (int cv = 0; cv < NC; ++cv) {
