@@ -71,9 +71,11 @@ struct Shape {
     // a chunk: the tile's planes of CH channels of one operand; channels l and
     // l + HP of it are a pair
     static constexpr int CH = 32, CK = CH / 16, NC = D / CH, HP = CH / 2;
-    static constexpr int kRaw = CH * 4 * kRow;              // words of a chunk's planes
+    // a copy: one chunk or two
+    static constexpr int PER = D < 64 ? 1 : 2, CC = PER * CH, NCC = D / CC;
+    static constexpr int kRaw = CC * 4 * kRow;              // words of a copy's planes
     static constexpr int kRawScales = D * kTileBlocks;      // halves of a tile's scales, of K or V
-    static constexpr int kRing = 4;
+    static constexpr int kRing = 4 / PER;
     static constexpr int kCodes = NB * CH * 8;              // words of a warp's codes of a chunk
     static constexpr int kOwn = kCodes > kPairs * D ? kCodes : kPairs * D;   // or of its partial outputs
     static constexpr int kScales = 2 * NB * D;              // halves: K, V; block; channels, pair by pair
@@ -286,7 +288,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                     unsigned int* status) {
     using Sh = Shape<D, NT, F32, NB>;
     constexpr int kTile = Sh::kTile;
-    constexpr int KS = Sh::KS, CH = Sh::CH, CK = Sh::CK, NC = Sh::NC, HP = Sh::HP, kPairs = Sh::kPairs, kRing = Sh::kRing;
+    constexpr int KS = Sh::KS, CH = Sh::CH, CK = Sh::CK, NC = Sh::NC, HP = Sh::HP, PER = Sh::PER, CC = Sh::CC, NCC = Sh::NCC, kPairs = Sh::kPairs, kRing = Sh::kRing;
     extern __shared__ uint32_t smem_raw[];
     uint32_t* s_raw = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u) / 4;   // the next 1024-byte boundary
     // [ring][plane][channel][row of the tile], 16-byte pieces swizzled by the channel
@@ -303,16 +305,16 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
     uint64_t* s_read = s_full + kRing + 1;              // every warp has read it
 
     const int ub = run_start(map.at, blockIdx.x);
-    const int units = run_start(map.at, blockIdx.x + 1) - ub, chunks = units * (2 * NC);
+    const int units = run_start(map.at, blockIdx.x + 1) - ub, copies = units * (2 * NCC);
     const int G = Hq / Hkv, C = T * G;
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int lg = lane >> 2, lt = lane & 3;            // g and t of the operand layouts
 
-    // copies chunk c of a unit (NC chunks of K, then NC of V) of row r to ring buffer i
+    // issues copy c of a unit (NCC of K, then NCC of V) of row r to ring buffer i
     auto copy = [&](const Row& r, int unit, int c, int i) {
         barrier_expect(s_full + i, 4 * Sh::kRaw);
-        copy_planes(s_raw + i * Sh::kRaw, c < NC ? &map.k[r.s] : &map.v[r.s], (unit - r.u0) * (kTile / 32),
-                    r.g * D + (c < NC ? c : c - NC) * CH, s_full + i);
+        copy_planes(s_raw + i * Sh::kRaw, c < NCC ? &map.k[r.s] : &map.v[r.s], (unit - r.u0) * (kTile / 32),
+                    r.g * D + (c < NCC ? c : c - NCC) * CC, s_full + i);
     };
     auto copy_scale = [&](const Row& r, int unit) {
         const int b = (unit - r.u0) * (kTile / kBlock);
@@ -333,9 +335,9 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         pdl_wait();
         if (lane == kRing) {
             copy_scale(rw, ub);
-        } else if (lane < kRing && lane < chunks) {
-            const int unit = ub + lane / (2 * NC);
-            copy(unit < rw.u1 ? rw : row_of(map.at, unit, Hkv, sets), unit, lane % (2 * NC), lane);
+        } else if (lane < kRing && lane < copies) {
+            const int unit = ub + lane / (2 * NCC);
+            copy(unit < rw.u1 ? rw : row_of(map.at, unit, Hkv, sets), unit, lane % (2 * NCC), lane);
         }
     }
 
@@ -470,12 +472,13 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 }
             // chunk c of the tile, of K or of V: its planes of the warp's blocks to registers, as codes to the
             // warp's own memory
-            auto stage = [&](bool isk, int c) {
-                const int rj = (2 * NC) % kRing == 0 ? c % kRing : j % kRing;
-                const uint32_t turn = (uint32_t)((2 * NC) % (2 * kRing) == 0 ? c / kRing : j / kRing) & 1;
-                barrier_wait(s_full + rj, turn, stuck);
+            auto stage = [&](bool isk, int chunk) {
+                const int c = chunk / PER, part_of = chunk % PER;   // its copy, and where in it
+                const int rj = (2 * NCC) % kRing == 0 ? c % kRing : j % kRing;
+                const uint32_t turn = (uint32_t)((2 * NCC) % (2 * kRing) == 0 ? c / kRing : j / kRing) & 1;
+                if (part_of == 0) barrier_wait(s_full + rj, turn, stuck);
                 // pieces of 16 bytes: a warp's two blocks of 128 keys, or the two warps' of 64 that share one
-                const uint32_t* src = s_raw + rj * Sh::kRaw + pl * Sh::kRow;
+                const uint32_t* src = s_raw + rj * Sh::kRaw + (part_of * CH + pl) * Sh::kRow;
                 const int piece = NB == 2 ? wp : wp / 2, swizzle = NB == 2 ? pl & 7 : (pl >> 1) & 3;
                 src += (piece ^ swizzle) * 4 + (NB == 2 ? 2 * part : 2 * (wp & 1) + part);
                 // both code layouts keep the lanes of a write, and of a read, on different banks
@@ -484,8 +487,8 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) P[e][k] = *reinterpret_cast<const uint2*>(src + (k * CH + e * HP) * Sh::kRow);
-                    barrier_arrive(s_read + rj);
+                        for (int k = 0; k < 4; ++k) P[e][k] = *reinterpret_cast<const uint2*>(src + (k * CC + e * HP) * Sh::kRow);
+                    if (part_of == PER - 1) barrier_arrive(s_read + rj);
                     uint32_t N[2][2][4];                // [channel][word][r]
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -516,8 +519,8 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) P[e][k] = src[(k * CH + e * HP) * Sh::kRow];
-                    barrier_arrive(s_read + rj);
+                        for (int k = 0; k < 4; ++k) P[e][k] = src[(k * CC + e * HP) * Sh::kRow];
+                    if (part_of == PER - 1) barrier_arrive(s_read + rj);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) planes_to_nibbles(P[e][0], P[e][1], P[e][2], P[e][3], N[e]);
                     uint32_t* dst = codes + (pl >> 3) * 128;
@@ -536,15 +539,15 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                     }
                 }
                 // warps take turns at the copy of the buffer's next chunk, once every warp has read this one
-                if (wp == ((2 * NC) % kWarps == 0 ? c : j) % kWarps && j + kRing < chunks) {
+                if (part_of == PER - 1 && wp == j % kWarps && j + kRing < copies) {
                     barrier_wait(s_read + rj, turn, stuck);
-                    const int cn = c + kRing, un = u + cn / (2 * NC);
+                    const int cn = c + kRing, un = u + cn / (2 * NCC);
                     if (lane == 0 && !stuck) {
-                        if (un < re) copy(rw, ub + un, cn % (2 * NC), rj);
-                        else copy(row_of(map.at, ub + un, Hkv, sets), ub + un, cn % (2 * NC), rj);
+                        if (un < re) copy(rw, ub + un, cn % (2 * NCC), rj);
+                        else copy(row_of(map.at, ub + un, Hkv, sets), ub + un, cn % (2 * NCC), rj);
                     }
                 }
-                ++j;
+                if (part_of == PER - 1) ++j;
                 __syncwarp();
             };
 #pragma unroll 1
@@ -930,7 +933,7 @@ bool tensor_maps(CUtensorMap* tm, CUtensorMap* stm, const uint32_t* planes, cons
     if (!encode) return false;
     const cuuint64_t row = (cuuint64_t)(n_pad / 8);
     const cuuint64_t dims[3] = {row / 4, (cuuint64_t)channels, 4}, strides[2] = {4 * row, row};
-    const cuuint32_t box[3] = {(cuuint32_t)tile / 32, 32, 4}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)tile / 32, (cuuint32_t)(d < 64 ? 32 : 64), 4}, step[3] = {1, 1, 1};
     const cuuint64_t sdims[2] = {(cuuint64_t)(n_pad / kBlock), (cuuint64_t)channels}, sstrides[1] = {(cuuint64_t)(n_pad / kBlock) * 2};
     const cuuint32_t sbox[2] = {(cuuint32_t)tile / kBlock, (cuuint32_t)d};
     return encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint32_t*>(planes), dims, strides, box, step,
