@@ -11,12 +11,12 @@
 // rows' tiles form one list, cut into equal runs, one per CTA, at most as many as
 // are resident; a run may end in the middle of a row, so every (CTA, row) pair
 // leaves a partial (o, m, l), and a second launch adds a row's partials in
-// order.  CTA p's partial of row r lies in slot p + r: a run that passes into
+// order (those of a short row are added in its cluster's shared memory).  CTA p's partial of row r lies in slot p + r: a run that passes into
 // the next row raises r, a row that passes into the next CTA raises p, so no
 // two meet.
 //
-// A tile.  Its planes arrive in chunks of 32 channels, K's then V's, by one
-// tensor copy each into a ring of four buffers: 128 bytes of every plane row, a
+// A tile.  Its planes arrive 64 channels at a time, K's then V's, by one tensor copy
+// each into a ring of two buffers: 128 bytes of every plane row, a
 // whole line (pieces of 64 bytes end at 3 TB/s, of 32 at 1.6).  Eight warps have
 // two blocks of 64 keys each, and no step of theirs waits for another warp
 // but the copy that reuses a buffer, which they issue in turn.  A warp turns the
@@ -44,9 +44,9 @@
 // to 2.6e-6).
 //
 // What bounds it: the instructions around the products, ALU and issue slots, not the
-// memory: 0.29 us per 64-key block and SM where the copies alone take 0.20; and
+// memory: 0.27 us per 64-key block and SM where the copies alone take 0.20; and
 // 13 us of launches, first copies and merge.  1048576 keys (4 heads of 128, 4 queries
-// each): 272 us, 4.2 TB/s; 131072: 47 us; 4096 keys of 1 head: 8.8 us.
+// each): 264 us, 4.3 TB/s; 131072: 46 us; 4096 keys of 1 head: 8.0 us.
 #include <cuda.h>
 
 #include "fathom_internal.cuh"
@@ -57,6 +57,7 @@ namespace {
 constexpr int kTilePairs = 4;                   // queries per 8 columns
 constexpr int kMaxCtas = 296;                   // two CTAs per SM
 
+constexpr int kMaxCluster = 8;                  // CTAs
 constexpr int kWarps = 8;                       // of a CTA
 constexpr int kThreads = 32 * kWarps;
 
@@ -106,7 +107,7 @@ template <int S>
 struct Spans {
     int nsess;
     int each, more;     // units of a CTA, and CTAs with one more
-    int pad;
+    int cluster;        // above 1: a row's tiles, one to a CTA of a cluster of this many
     Span span[S];
 };
 template <int S>
@@ -172,7 +173,7 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y, uint32_t mask) 
     return r;
 }
 
-// The ring of raw planes: a chunk's bytes arrive by one asynchronous tensor
+// The ring of raw planes: a buffer's bytes arrive by one asynchronous tensor
 // copy.  A wait gives up after 2^31 clocks, about a second, which no correct run
 // reaches; that warp then waits no more, issues no further copy, leaves time for
 // those in flight, and reports.
@@ -214,6 +215,17 @@ __device__ __forceinline__ void copy_scales(void* dst, const CUtensorMap* tm, in
             smem_addr(dst)),
         "l"(tm), "r"(block), "r"(channel), "r"(smem_addr(b))
         : "memory");
+}
+// a float of the same place in the shared memory of CTA `rank` of the cluster
+__device__ __forceinline__ float peer_float(const float* p, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // this warp has read what the barrier's buffer held
 __device__ __forceinline__ void barrier_arrive(uint64_t* b) {
@@ -301,7 +313,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
     float* s_m = reinterpret_cast<float*>(s_q2 + Sh::kQ2Words);   // [warp][pair]
     float* s_l = s_m + kWarps * kPairs;
     float* s_f = s_l + kWarps * kPairs;                 // [pair] the query's part of the logits' factor
-    uint64_t* s_full = reinterpret_cast<uint64_t*>(s_f + kPairs);   // [ring] the chunk has arrived; then the scales
+    uint64_t* s_full = reinterpret_cast<uint64_t*>(s_f + kPairs);   // [ring] the copy has arrived; then the scales
     uint64_t* s_read = s_full + kRing + 1;              // every warp has read it
 
     const int ub = run_start(map.at, blockIdx.x);
@@ -538,7 +550,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                         for (int r = 0; r < 4; ++r) d2[(r ^ ((pl >> 1) & 3)) * 2] = make_uint2(N[0][r], N[1][r]);
                     }
                 }
-                // warps take turns at the copy of the buffer's next chunk, once every warp has read this one
+                // warps take turns at the buffer's next copy, once every warp has read this one
                 if (part_of == PER - 1 && wp == j % kWarps && j + kRing < copies) {
                     barrier_wait(s_read + rj, turn, stuck);
                     const int cn = c + kRing, un = u + cn / (2 * NCC);
@@ -740,8 +752,22 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         }
         __syncthreads();
         float* part = slots + (int64_t)(blockIdx.x + rw.row) * (kPairs * (D + 2));
+        // a cluster's partials stay in shared memory, where the planes were
+        const bool together = NS == 1 && NB == 1 && map.at.cluster > 1;
+        if (together) part = reinterpret_cast<float*>(s_raw);
+        auto result = [&](int x, int c, float o, float M, float L) {
+            const int pr = rw.set * kPairs + x;
+            if (pr >= C) return;
+            const int64_t h = ((int64_t)s * T + pr / G) * Hq + rw.g * G + pr % G;
+            if (parts) {
+                parts[h * (D + 2) + c] = o;
+                if (c == 0) parts[h * (D + 2) + D] = M, parts[h * (D + 2) + D + 1] = L;
+            } else {
+                out[h * D + c] = L > 0.0f ? o / L : 0.0f;
+            }
+        };
         for (int e = threadIdx.x; e < kPairs * D; e += kThreads) {
-            const int x = e / D, c = e % D, pr = rw.set * kPairs + x;
+            const int x = e / D, c = e % D;
             float M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kPairs + x]);
@@ -757,15 +783,35 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
             if (!whole) {
                 part[e] = o;
                 if (c == 0) part[kPairs * D + x] = M, part[kPairs * (D + 1) + x] = L;
-            } else if (pr < C) {
-                const int64_t h = ((int64_t)s * T + pr / G) * Hq + rw.g * G + pr % G;
-                if (parts) {
-                    parts[h * (D + 2) + c] = o;
-                    if (c == 0) parts[h * (D + 2) + D] = M, parts[h * (D + 2) + D + 1] = L;
-                } else {
-                    out[h * D + c] = L > 0.0f ? o / L : 0.0f;
-                }
+            } else {
+                result(x, c, o, M, L);
             }
+        }
+        if (together) {
+            cluster_sync();
+            const int cl = map.at.cluster;
+            for (int e = (blockIdx.x % cl) * kThreads + threadIdx.x; e < kPairs * D; e += cl * kThreads) {
+                const int x = e / D;
+                float mp[kMaxCluster], lp[kMaxCluster], op[kMaxCluster], M = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kMaxCluster; ++i) {
+                    const bool in = i < cl;
+                    op[i] = in ? peer_float(part + e, i) : 0.0f;
+                    mp[i] = in ? peer_float(part + kPairs * D + x, i) : -INFINITY;
+                    lp[i] = in ? peer_float(part + kPairs * (D + 1) + x, i) : 0.0f;
+                    M = fmaxf(M, mp[i]);
+                }
+                const float Mb = M == -INFINITY ? 0.0f : M;
+                float L = 0.0f, o = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kMaxCluster; ++i) {
+                    const float f = ex2(mp[i] - Mb);
+                    L = fmaf(lp[i], f, L);
+                    o = fmaf(op[i], f, o);
+                }
+                result(x, e % D, o, M, L);
+            }
+            cluster_sync();                             // until the others have read this CTA's
         }
         __syncthreads();                                // before the next row's queries and codes
         if (u < units) rw = row_of(map.at, ub + u, Hkv, sets);
@@ -913,10 +959,17 @@ struct Call {
     Spans<kAttendSets> at;
     int P;
     bool shared;   // some row's keys may be shared by several CTAs, or a row has none
+
+    // tiles of a row of session s
+    int tiles(int s, int tile) const {
+        const int64_t last = map.visible[s] + T - 1;   // keys that the last token sees
+        const int64_t keys = last < map.n[s] ? (last > 0 ? last : 0) : map.n[s];
+        return (int)((keys + tile - 1) / tile);
+    }
 };
 
 // The tensor maps of a store: planes as words, channels of all heads, planes, a box
-// being a tile's 128 bytes of a chunk's channels and all planes, 16-byte pieces
+// being a tile's 128 bytes of a copy's channels and all planes, 16-byte pieces
 // of each row swizzled by the row number; scales as blocks, channels of all
 // heads, a box being a tile's blocks of a head's channels.
 bool tensor_maps(CUtensorMap* tm, CUtensorMap* stm, const uint32_t* planes, const uint16_t* scales, int channels, int d,
@@ -944,17 +997,15 @@ bool tensor_maps(CUtensorMap* tm, CUtensorMap* stm, const uint32_t* planes, cons
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Lays the sessions out in tiles; the number of units.
-int lay_out(Call& a, int tile) {
+// Lays the sessions out in tiles, each row's number a multiple of `granule`; the number of units.
+int lay_out(Call& a, int tile, int granule) {
     int64_t U = 0;
     for (int s = 0; s < a.map.nsess; ++s) {
-        const int64_t last = a.map.visible[s] + a.T - 1;   // keys that the last token sees
-        const int64_t keys = last < a.map.n[s] ? (last > 0 ? last : 0) : a.map.n[s];
         Span& sp = a.at.span[s];
         sp.n = (int)a.map.n[s];
         sp.visible = (int)a.map.visible[s];
         sp.unit0 = (int)U;
-        sp.tiles = (int)((keys + tile - 1) / tile);
+        sp.tiles = (a.tiles(s, tile) + granule - 1) / granule * granule;
         U += (int64_t)sp.tiles * a.Hkv * a.sets;
         a.shared = a.shared || sp.tiles != 1;
     }
@@ -965,15 +1016,23 @@ template <int D, int NT, bool F32, int NS, int NB>
 cudaError_t launch_shape(Call& a) {
     using Sh = Shape<D, NT, F32, NB>;
     static_assert(Sh::kCtas * (Sh::kSmem + 1024) <= kMaxSmem + 1024, "the CTAs of an SM fit");
+    // a row of 2 to 8 half tiles: one cluster, which adds its partials itself (4096 keys, 1 head of 128:
+    // 8.0 us against 9.1 with a second launch; 32 heads: 11.2 against 13.6; 16 heads: 10.6 against 10.1)
+    int cluster = 1;
+    if (NS == 1 && NB == 1)
+        while (cluster < a.tiles(0, Sh::kTile)) cluster *= 2;
+    if (cluster > kMaxCluster) cluster = 1;
     a.shared = false;
-    const int U = lay_out(a, Sh::kTile);
-    a.P = U < 148 * Sh::kCtas ? U : 148 * Sh::kCtas;
+    const int U = lay_out(a, Sh::kTile, cluster);
+    a.P = U < 148 * Sh::kCtas || cluster > 1 ? U : 148 * Sh::kCtas;
     a.at.each = U / a.P;
     a.at.more = U % a.P;
     Sessions<NS> m;
     m.at.nsess = a.at.nsess;
     m.at.each = a.at.each;
     m.at.more = a.at.more;
+    m.at.cluster = cluster;
+    a.shared = a.shared && cluster == 1;
     for (int s = 0; s < a.at.nsess; ++s) {
         m.at.span[s] = a.at.span[s];
         if (!tensor_maps(&m.k[s], &m.ks[s], a.map.k_planes[s], a.map.k_scales[s], a.Hkv * D, D, a.map.k_pad[s], Sh::kTile) ||
@@ -983,7 +1042,7 @@ cudaError_t launch_shape(Call& a) {
     auto kern = store_attend_kernel<D, NT, F32, NS, NB>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, true, 1, m, a.q, a.q_dtype, a.T, a.Hq, a.Hkv,
+    return launch_ex(kern, dim3(a.P), dim3(kThreads), Sh::kSmem, a.stream, true, cluster, m, a.q, a.q_dtype, a.T, a.Hq, a.Hkv,
                      a.sets, a.slots, a.out, a.parts, device_status_ptr());
 }
 
@@ -1008,10 +1067,22 @@ cudaError_t launch_dim(int nt, Call& a, int units) {
 cudaError_t launch_store_attend(const AttendMap& map, int Hkv, int d, const void* q, int q_dtype, int T, int Hq, float* out,
                                 float* parts, void* ws, cudaStream_t stream) {
     const int64_t C = (int64_t)T * (Hq / Hkv);
-    const int nt = tiles_of_set(C), pairs = nt * kTilePairs;
-    Call a{map, q, q_dtype, T, Hq, Hkv, (int)((C + pairs - 1) / pairs), static_cast<float*>(ws), out, parts, stream, {}, 0, false};
+    int nt = tiles_of_set(C);
+    Call a{map, q, q_dtype, T, Hq, Hkv, 0, static_cast<float*>(ws), out, parts, stream, {}, 0, false};
     a.at.nsess = map.nsess;
-    const int units = lay_out(a, 1024);
+    a.sets = (int)((C + kTilePairs - 1) / kTilePairs);
+    int units = lay_out(a, 1024, 1);
+    // few keys and many queries: sets of 4, while each half tile has an SM of its own, or half of one in the
+    // cluster of a short row (1 head of 128, 8 queries, 4096 keys: 8.0 us against 10.3; 16 heads: 11.1
+    // against 14.3; 8 heads, 9000 keys, where two would share an SM: 13.9 against 12.6)
+    const bool cluster = map.nsess == 1 && a.tiles(0, 512) <= kMaxCluster && d <= 128;
+    if (map.nsess > 1 || 2 * units > 148 * (cluster ? 2 : 1)) {
+        a.sets = (int)((C + nt * kTilePairs - 1) / (nt * kTilePairs));
+        units = lay_out(a, 1024, 1);
+    } else {
+        nt = 1;
+    }
+    const int pairs = nt * kTilePairs;
     if (units > 0) {
         cudaError_t e;
         switch (d) {

@@ -485,3 +485,37 @@ def test_long_sums_are_not_biased(n, d, G):
     out = F.store_attend(ks, vs, q).double().cpu().numpy()
     assert np.linalg.norm(out - ref) <= 2.0 ** -18 * np.linalg.norm(ref)
     assert abs((out - ref).mean()) <= 2.0 ** -18 * np.abs(ref).mean()
+
+
+@pytest.mark.parametrize("G,T,d,dtype", [(1, 1, 128, torch.float32), (4, 1, 32, torch.bfloat16), (8, 1, 128, torch.bfloat16),
+                                         (8, 1, 256, torch.float32), (2, 5, 64, torch.bfloat16)])
+@pytest.mark.parametrize("n", [513, 1024, 1025, 1537, 2049, 2561, 3584, 3585, 4096, 4097])
+def test_short_rows_of_one_cluster(n, G, T, d, dtype):
+    """2 to 8 half tiles to a row, some of a cluster's CTAs without any; and the row's partials."""
+    ks, vs = make_store(n, 2, d, n, garbage=True), make_store(n, 2, d, n + 1, garbage=True)
+    q = queries((T, 2 * G, d), n % 89, dtype)
+    ref, tol, M, L = reference(ks, vs, q, n - T + 1)
+    check(F.store_attend(ks, vs, q), ref, tol)
+    parts = F.store_attend_partial(ks, vs, q, n - T + 1).double().cpu().numpy()
+    assert (parts[..., d] >= M - 1e-4).all() and (parts[..., d] < M + 1 + 1e-4).all()
+    check(torch.from_numpy(parts[..., :d] / parts[..., d + 1:]), ref, tol)
+
+
+@pytest.mark.parametrize("T", [600, 1500])
+def test_short_rows_whose_tokens_see_few_tiles(T):
+    """Sets of tokens before the first key, in its tile, and behind: CTAs of a cluster that see nothing."""
+    n = 1400
+    ks, vs = make_store(n, 1, 32, T), make_store(n, 1, 32, T + 1)
+    q = queries((T, 1, 32), T)
+    ref, tol, _, _ = reference(ks, vs, q, n - T + 1)
+    check(F.store_attend(ks, vs, q), ref, tol)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_sets_of_eight_in_half_tiles(d, dtype):
+    n = 9300
+    ks, vs = make_store(n, 4, d, d), make_store(n, 4, d, d + 1)
+    q = queries((32, d), d, dtype)
+    ref, tol, _, _ = reference(ks, vs, q[None], n)
+    check(F.store_attend(ks, vs, q), ref, tol)
