@@ -355,3 +355,31 @@ def test_calls_behind_copies_memsets_and_other_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out2, out) and torch.equal(q2, q) and torch.equal(ks2.planes, ks.planes)
+
+
+def test_offsets_beyond_32_bits():
+    """A small cache and the same keys in arrays whose later heads lie beyond 2^32 bytes and 2^31 elements: same bits."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    Hkv, Hq, d, T, n = 4, 8, 256, 900, 900
+    g = torch.Generator(device=DEV).manual_seed(23)
+    qkv = torch.randn(T, Hq + 2 * Hkv, d, device=DEV, generator=g).bfloat16()
+    got = []
+    for rows_n, cap in ((1024, 1024), (1 << 22, 1 << 24)):
+        rows = torch.empty(2, Hkv, rows_n, d, dtype=torch.bfloat16, device=DEV)
+        stores = []
+        for _ in range(2):
+            stores.append(F.Store(torch.empty(Hkv, d, 4, cap // 32, dtype=torch.int32, device=DEV),
+                                  torch.empty(Hkv, d, cap // 64, dtype=torch.int16, device=DEV), 0))
+        ks, vs = stores
+        q = F.qk_norm_rope(qkv, Hq, Hkv, freqs(d), rows[0], rows[1], 0)
+        F.append_rows(ks, vs, rows[0], rows[1], n)
+        out = F.store_attend(ks, vs, q[-1])
+        several = F.store_attend_batched([ks, ks], [vs, vs], q[-4:].reshape(2, 2, Hq, d))
+        got.append((q, rows[:, :, :n].clone(), *(st.planes[..., :30].clone() for st in stores), out, several))
+        assert torch.isfinite(out).all() and out.abs().max() > 0
+        torch.cuda.synchronize()
+        del rows, stores, ks, vs
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    torch.cuda.empty_cache()

@@ -519,3 +519,26 @@ def test_sets_of_eight_in_half_tiles(d, dtype):
     q = queries((32, d), d, dtype)
     ref, tol, _, _ = reference(ks, vs, q[None], n)
     check(F.store_attend(ks, vs, q), ref, tol)
+
+
+def test_calls_from_several_threads():
+    """Host threads with a stream each, short and long rows at once."""
+    from concurrent.futures import ThreadPoolExecutor
+    work = []
+    for i, n in enumerate((700, 3000, 9000, 60000)):
+        ks, vs = make_store(n, 2, 64, i), make_store(n, 2, 64, i + 10)
+        q = queries((16, 64), i)
+        work.append((ks, vs, q, F.store_attend(ks, vs, q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def go(w):
+        ks, vs, q, _, stream = w
+        with torch.cuda.device(DEV):
+            outs = [F.store_attend(ks, vs, q, stream=stream) for _ in range(50)]
+            stream.synchronize()
+        return outs
+
+    with ThreadPoolExecutor(4) as pool:
+        for w, outs in zip(work, pool.map(go, work)):
+            assert all(torch.equal(o, w[3]) for o in outs)
+    assert F.last_device_status() == 0
