@@ -472,7 +472,8 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
  *   K, V      stores with the same n, Hkv, d, n < 2^31 - 8192; each device- or
  *             host-resident; n may be 0.
  *   q         device, [n_tokens][Hq][d], FATHOM_F32 or FATHOM_BF16, finite values, the
- *             largest times the largest scale below 2^112; 1 <= n_tokens <= 4096 (made
+ *             largest times the largest scale below 2^112 (a NaN makes its head's output
+ *             NaN, or 0 where the token sees no key, and no other's); 1 <= n_tokens <= 4096 (made
  *             for few tokens: the stores are read again for every 8 (token, head of a
  *             group) pairs).
  *   out       device, f32 [n_tokens][Hq][d].
@@ -500,7 +501,8 @@ int fathom_store_attend(const fathom_store* K, const fathom_store* V, const void
  *             negative or 0 for a range behind the tokens, >= n for all keys).
  *   parts     device, f32 [n_tokens][Hq][d + 2], as fathom_sparse_attend_partial
  *             writes them; the two kinds may be merged with each other.  m is a whole number,
- *             above the largest score (in log2 units) by less than 1.
+ *             above the largest score (in log2 units) by less than 1.  A NaN in a query leaves o and l
+ *             NaN and m -inf, as it does there; fathom_attend_merge gives 0 for such a head.
  */
 int fathom_store_attend_partial(const fathom_store* K, const fathom_store* V, const void* q, int q_dtype, int n_tokens,
                                 int n_q_heads, int64_t visible, float* parts, void* workspace, size_t workspace_bytes,
