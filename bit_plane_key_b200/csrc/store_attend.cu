@@ -49,6 +49,8 @@
 // each): 264 us, 4.3 TB/s; 131072: 46 us; 4096 keys of 1 head: 8.0 us.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "fathom_internal.cuh"
 
 namespace fathom {
@@ -958,6 +960,7 @@ struct Call {
     cudaStream_t stream;
     Spans<kAttendSets> at;
     int P;
+    int pairs;     // of a set
     bool shared;   // some row's keys may be shared by several CTAs, or a row has none
 
     // tiles of a row of session s
@@ -1012,16 +1015,61 @@ int lay_out(Call& a, int tile, int granule) {
     return (int)U;
 }
 
+// Clusters of 2, 4 or 8 CTAs of the half tiles' kernel that the current device holds at once (an SM group's
+// last SMs may not make a whole one: B200, two CTAs to an SM: 148, 71, 33; one: 74, 33, 15); a device is asked once.
+template <int D, int NT, bool F32>
+int resident_clusters(int cluster) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][kMaxCluster + 1];   // the number and 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+    std::atomic<int>& at = known[dev][cluster];
+    int held = at.load(std::memory_order_relaxed) - 1;
+    if (held < 0) {
+        using Sh = Shape<D, NT, F32, 1>;
+        auto kern = store_attend_kernel<D, NT, F32, 1, 1>;
+        cudaLaunchAttribute size;
+        size.id = cudaLaunchAttributeClusterDimension;
+        size.val.clusterDim.x = (unsigned)cluster;
+        size.val.clusterDim.y = size.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(cluster);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Sh::kSmem;
+        cfg.attrs = &size;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&held, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        at.store(held + 1, std::memory_order_relaxed);
+    }
+    return held;
+}
+
+// CTAs of the cluster that takes a row of 2 to 8 half tiles and adds its partials itself, or 1: each tile by itself
+// and a second launch, which costs 1.2 us.  Clusters that are not all resident take a second turn (1 query a head,
+// 2049 keys, 40 heads of 128: 18.2 us against 11.9; 16 heads of 256: 25.4 against 14.1).  Some 64 CTAs in clusters
+// of 4 and 8 lie two to an SM, which heads of 128 feel: there the second launch is shorter as long as it leaves an SM
+// to each tile (4096 keys, 8 heads: 8.5 us against 9.1; 12: 10.1 against 9.2; 16: 10.2 against 9.8; 20: 10.5 against
+// 11.8; heads of 64: 5.8 against 6.8, 6.7 against 6.9, 6.8 against 7.7, 7.0 against 8.6).
+template <int D, int NT, bool F32>
+int cluster_of(const Call& a) {
+    const int tiles = a.tiles(0, Shape<D, NT, F32, 1>::kTile), rows = a.Hkv * a.sets;
+    if (tiles < 2 || tiles > kMaxCluster) return 1;
+    int cluster = 2;
+    while (cluster < tiles) cluster *= 2;
+    if (D == 128 && cluster > 2 && (int64_t)rows * cluster > 64 && (int64_t)rows * tiles <= 148) return 1;
+    return rows <= resident_clusters<D, NT, F32>(cluster) ? cluster : 1;
+}
+
 template <int D, int NT, bool F32, int NS, int NB>
 cudaError_t launch_shape(Call& a) {
     using Sh = Shape<D, NT, F32, NB>;
     static_assert(Sh::kCtas * (Sh::kSmem + 1024) <= kMaxSmem + 1024, "the CTAs of an SM fit");
-    // a row of 2 to 8 half tiles: one cluster, which adds its partials itself (4096 keys, 1 head of 128:
-    // 8.0 us against 9.1 with a second launch; 32 heads: 11.2 against 13.6; 16 heads: 10.6 against 10.1)
     int cluster = 1;
-    if (NS == 1 && NB == 1)
-        while (cluster < a.tiles(0, Sh::kTile)) cluster *= 2;
-    if (cluster > kMaxCluster) cluster = 1;
+    if constexpr (NS == 1 && NB == 1) cluster = cluster_of<D, NT, F32>(a);
     a.shared = false;
     const int U = lay_out(a, Sh::kTile, cluster);
     a.P = U < 148 * Sh::kCtas || cluster > 1 ? U : 148 * Sh::kCtas;
@@ -1055,47 +1103,47 @@ cudaError_t launch_type(Call& a, int units) {
     return launch_shape<D, NT, F32, 1, 2>(a);
 }
 
-template <int D>
-cudaError_t launch_dim(int nt, Call& a, int units) {
-    const bool f32 = a.q_dtype == FATHOM_F32;
-    if (nt == 1) return f32 ? launch_type<D, 1, true>(a, units) : launch_type<D, 1, false>(a, units);
-    return f32 ? launch_type<D, 2, true>(a, units) : launch_type<D, 2, false>(a, units);
+template <int D, bool F32>
+cudaError_t launch_dim(Call& a) {
+    const int64_t C = (int64_t)a.T * (a.Hq / a.Hkv);
+    a.pairs = kTilePairs;
+    a.sets = (int)((C + kTilePairs - 1) / kTilePairs);
+    int units = lay_out(a, 1024, 1);
+    if (tiles_of_set(C) == 2) {
+        // few keys and many queries: sets of 4, while each half tile has an SM of its own, or half of one in the
+        // cluster of a short row (1 head of 128, 8 queries, 4096 keys: 8.0 us against 10.3; 16 heads: 11.0
+        // against 14.2; 8 heads, 9000 keys, where two would share an SM: 13.9 against 12.6; 24 heads, 3000 keys,
+        // whose clusters would not all be resident: 14.7 against 13.3)
+        const bool alone = 2 * units <= 148 || (D <= 128 && (int64_t)a.Hkv * a.sets * a.tiles(0, 512) <= 148);
+        const bool together = D <= 128 && 2 * units <= 2 * 148 && (a.tiles(0, 512) == 1 || cluster_of<D, 1, F32>(a) > 1);
+        if (a.map.nsess > 1 || (!alone && !together)) {
+            a.pairs = 2 * kTilePairs;
+            a.sets = (int)((C + a.pairs - 1) / a.pairs);
+            units = lay_out(a, 1024, 1);
+        }
+    }
+    if (units == 0) return cudaSuccess;
+    return a.pairs == kTilePairs ? launch_type<D, 1, F32>(a, units) : launch_type<D, 2, F32>(a, units);
 }
 
 }  // namespace
 
 cudaError_t launch_store_attend(const AttendMap& map, int Hkv, int d, const void* q, int q_dtype, int T, int Hq, float* out,
                                 float* parts, void* ws, cudaStream_t stream) {
-    const int64_t C = (int64_t)T * (Hq / Hkv);
-    int nt = tiles_of_set(C);
-    Call a{map, q, q_dtype, T, Hq, Hkv, 0, static_cast<float*>(ws), out, parts, stream, {}, 0, false};
+    Call a{map, q, q_dtype, T, Hq, Hkv, 0, static_cast<float*>(ws), out, parts, stream, {}, 0, 0, true};
     a.at.nsess = map.nsess;
-    a.sets = (int)((C + kTilePairs - 1) / kTilePairs);
-    int units = lay_out(a, 1024, 1);
-    // few keys and many queries: sets of 4, while each half tile has an SM of its own, or half of one in the
-    // cluster of a short row (1 head of 128, 8 queries, 4096 keys: 8.0 us against 10.3; 16 heads: 11.1
-    // against 14.3; 8 heads, 9000 keys, where two would share an SM: 13.9 against 12.6)
-    const bool cluster = map.nsess == 1 && a.tiles(0, 512) <= kMaxCluster && d <= 128;
-    if (map.nsess > 1 || 2 * units > 148 * (cluster ? 2 : 1)) {
-        a.sets = (int)((C + nt * kTilePairs - 1) / (nt * kTilePairs));
-        units = lay_out(a, 1024, 1);
-    } else {
-        nt = 1;
+    const bool f32 = q_dtype == FATHOM_F32;
+    cudaError_t e;
+    switch (d) {
+        case 32: e = f32 ? launch_dim<32, true>(a) : launch_dim<32, false>(a); break;
+        case 64: e = f32 ? launch_dim<64, true>(a) : launch_dim<64, false>(a); break;
+        case 128: e = f32 ? launch_dim<128, true>(a) : launch_dim<128, false>(a); break;
+        case 256: e = f32 ? launch_dim<256, true>(a) : launch_dim<256, false>(a); break;
+        default: return cudaErrorInvalidValue;
     }
-    const int pairs = nt * kTilePairs;
-    if (units > 0) {
-        cudaError_t e;
-        switch (d) {
-            case 32: e = launch_dim<32>(nt, a, units); break;
-            case 64: e = launch_dim<64>(nt, a, units); break;
-            case 128: e = launch_dim<128>(nt, a, units); break;
-            case 256: e = launch_dim<256>(nt, a, units); break;
-            default: return cudaErrorInvalidValue;
-        }
-        if (e != cudaSuccess || !a.shared) return e;
-    }
-    return launch_ex(store_attend_merge_kernel, dim3((unsigned)((int64_t)map.nsess * Hkv * a.sets * pairs)),
-                     dim3(kMergeThreads), 0, stream, a.P > 0, 1, a.at, a.slots, T, Hq, Hkv, a.sets, pairs, d, out, parts);
+    if (e != cudaSuccess || !a.shared) return e;
+    return launch_ex(store_attend_merge_kernel, dim3((unsigned)((int64_t)map.nsess * Hkv * a.sets * a.pairs)),
+                     dim3(kMergeThreads), 0, stream, a.P > 0, 1, a.at, a.slots, T, Hq, Hkv, a.sets, a.pairs, d, out, parts);
 }
 
 }  // namespace fathom

@@ -1,4 +1,5 @@
-"""Attention over stores (fathom_store_attend, _batched, _partial) at its edges: a query that is not a number."""
+"""Attention over stores (fathom_store_attend, _batched, _partial) at its edges: a query that is not a number, short rows on
+both sides of what the device holds of clusters."""
 import math
 
 import pytest
@@ -10,7 +11,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 from bit_plane_key_b200 import fathom as F  # noqa: E402
-from test_gpu_store_attend import make_store, queries  # noqa: E402
+from test_gpu_store_attend import check, make_store, queries, reference  # noqa: E402
 
 DEV = torch.device("cuda:0")
 
@@ -41,3 +42,51 @@ def test_a_nan_query_that_sees_no_key_gets_zero():
     q = queries((5, 2, 64), 3)
     q[0] = math.nan
     assert (F.store_attend(ks, vs, q)[:3] == 0).all()
+
+
+@pytest.mark.parametrize("Hkv,d,G,n", [(8, 128, 1, 4096), (9, 128, 1, 4096), (18, 128, 1, 4096), (19, 128, 1, 4096), (33, 128, 1, 2100),
+                                       (34, 128, 4, 2100), (49, 128, 1, 2049), (29, 128, 2, 2049), (16, 128, 4, 1100),
+                                       (17, 128, 4, 1100), (71, 64, 1, 1100), (72, 64, 1, 1100), (33, 64, 4, 4096),
+                                       (34, 32, 1, 2049), (15, 256, 1, 2100), (16, 256, 4, 2100), (33, 256, 1, 1500),
+                                       (34, 256, 1, 1500), (8, 256, 8, 2049), (20, 128, 8, 2049), (24, 128, 8, 3000),
+                                       (24, 64, 8, 2049), (40, 128, 8, 2049), (16, 256, 8, 3000), (24, 128, 8, 1500)])
+def test_short_rows_of_many_heads(Hkv, d, G, n):
+    """Where a row's CTAs are a cluster and where they are not: as many as the device holds, one more, sets of 4 and of 8."""
+    ks, vs = make_store(n, Hkv, d, n, garbage=True), make_store(n, Hkv, d, n + 1, garbage=True)
+    q = queries((1, Hkv * G, d), d)
+    ref, tol, _, _ = reference(ks, vs, q, n)
+    check(F.store_attend(ks, vs, q), ref, tol)
+    assert F.last_device_status() == 0
+
+
+def _fastest(calls):
+    """us of each call, the fastest of many replays of 20, taken in turn."""
+    graphs, best = [], [math.inf] * len(calls)
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(20):
+                call()
+        graphs.append(g)
+    for _ in range(30):
+        for i, g in enumerate(graphs):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record(), g.replay(), b.record()
+            torch.cuda.synchronize()
+            best[i] = min(best[i], a.elapsed_time(b) * 50)
+    return best
+
+
+@pytest.mark.parametrize("d,G,n,few,many", [(128, 1, 2049, 32, 40), (128, 8, 2049, 16, 20), (256, 1, 2049, 14, 18), (64, 8, 3000, 16, 20)])
+def test_no_short_row_waits_for_a_second_turn(d, G, n, few, many):
+    """A quarter more heads cost no second turn of the GPU: clusters that are not all resident took 1.6 to 1.9 times as long."""
+    calls = []
+    for Hkv in (few, many):
+        ks, vs, q = make_store(n, Hkv, d, 1), make_store(n, Hkv, d, 2), queries((Hkv * G, d), 3)
+        out = torch.empty(Hkv * G, d, device=DEV)
+        ws = torch.empty(F.store_attend_workspace_bytes(ks, 1, 1, Hkv * G), dtype=torch.uint8, device=DEV)
+        calls.append(lambda ks=ks, vs=vs, q=q, out=out, ws=ws: F.store_attend(ks, vs, q, out=out, workspace=ws))
+    a, b = _fastest(calls)
+    assert b < 1.4 * a, (a, b)
