@@ -51,6 +51,7 @@
 
 #include <atomic>
 
+#include "barrier.cuh"
 #include "fathom_internal.cuh"
 
 namespace fathom {
@@ -175,35 +176,7 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y, uint32_t mask) 
     return r;
 }
 
-// The ring of raw planes: a buffer's bytes arrive by one asynchronous tensor
-// copy.  A wait gives up after 2^31 clocks, about a second, which no correct run
-// reaches; that warp then waits no more, issues no further copy, leaves time for
-// those in flight, and reports.
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void barrier_init(uint64_t* b, int count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ bool barrier_try(uint64_t* b, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(done)
-                 : "r"(smem_addr(b)), "r"(parity)
-                 : "memory");
-    return done != 0;
-}
-__device__ __noinline__ bool barrier_gives_up(uint64_t* b, uint32_t parity) {
-    const uint32_t start = (uint32_t)clock();
-    while ((uint32_t)clock() - start < 1u << 31)
-        if (barrier_try(b, parity)) return false;
-    return true;
-}
-__device__ __forceinline__ void barrier_wait(uint64_t* b, uint32_t parity, bool& stuck) {
-    if (!barrier_try(b, parity) && !stuck) stuck = barrier_gives_up(b, parity);
-}
-// bytes to come before the barrier's phase is over
-__device__ __forceinline__ void barrier_expect(uint64_t* b, uint32_t bytes) {
-    asm volatile("{ .reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1; }" ::"r"(smem_addr(b)), "r"(bytes) : "memory");
-}
+// The ring of raw planes: a buffer's bytes arrive by one asynchronous tensor copy.
 __device__ __forceinline__ void copy_planes(void* dst, const CUtensorMap* tm, int word, int channel, uint64_t* b) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -229,13 +202,6 @@ __device__ __forceinline__ float peer_float(const float* p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// this warp has read what the barrier's buffer held
-__device__ __forceinline__ void barrier_arrive(uint64_t* b) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0)
-        asm volatile("{ .reg .b64 t; mbarrier.arrive.shared::cta.b64 t, [%0]; }" ::"r"(smem_addr(b)) : "memory");
-}
-
 // plane words W[j] of 32 keys -> N[r]: nibble m = code of key 4 m + r
 __device__ __forceinline__ void planes_to_nibbles(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t* N) {
     const uint32_t E = pick(w0 << 1, w1, 0xAAAAAAAAu), O = pick(w0, w1 >> 1, 0xAAAAAAAAu);
@@ -818,11 +784,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         __syncthreads();                                // before the next row's queries and codes
         if (u < units) rw = row_of(map.at, ub + u, Hkv, sets);
     }
-    if (stuck) {
-        const uint32_t start = (uint32_t)clock();
-        while ((uint32_t)clock() - start < 1u << 31) {}
-        atomicOr(status, (unsigned)FATHOM_DEV_TIMEOUT);
-    }
+    barrier_report(stuck, status);
 }
 
 // One CTA per (row, pair) whose keys were shared by several CTAs, or that has

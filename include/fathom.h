@@ -484,6 +484,8 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
  * that the stores had when it was captured.  The call's kernels are
  * launched with programmatic serialization: they are scheduled while the kernel
  * before them in the stream finishes, and wait for it before they read or write.
+ * When fathom_last_device_status() has FATHOM_DEV_TIMEOUT, what the calls since it was
+ * last read wrote is undefined (a copy did not arrive within a second).
  * Errors: EINVAL for null pointers, bad sizes, stores that differ, arrays not on
  * this device or not where host_resident says; ENOMEM for a short workspace;
  * EUNSUPPORTED for d other than 32, 64, 128, 256, and for more work than 2^26
