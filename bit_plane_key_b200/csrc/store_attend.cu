@@ -41,7 +41,9 @@
 // the offset is; what is cut off the low halves' sums is 2^-10 smaller.  The running
 // maximum is rounded up to a whole number of binary orders: what was summed
 // is rescaled exactly.  Against 64 bits: 2e-7 to 7e-7 of the output (fp32 arithmetic: 2e-7
-// to 2.6e-6).
+// to 2.6e-6).  The halves are fixed point: their last place is that of the head's largest |q|
+// times the block's largest Delta (2^-24 of it), so where those two do not meet in one
+// channel, logits lose bits that fp32 would keep.
 //
 // What bounds it: the instructions around the products, ALU and issue slots, not the
 // memory: 0.27 us per 64-key block and SM where the copies alone take 0.20; and

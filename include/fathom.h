@@ -467,6 +467,13 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
  *   out[t][h] = softmax_i(q[t][h] . K_i / sqrt(d)) V_i over the keys i that token t
  *   sees, K_ic = Delta_c (code_ic - 7.5) in the block scale Delta, V likewise,
  *   fp32 accumulation; 0 for a token that sees no key.
+ * The products run on the matrix units, their operands in two fp16 halves: a factor
+ * q_c Delta_c is off by at most 2^-21 of itself plus 2^-24 of the largest |q| of the head times
+ * the largest Delta of the block, a weight by 2^-23 of the block's largest weight (or 2^-35 of all).
+ * That is at or below what fp32 arithmetic loses as long as a head's largest |q|
+ * and the largest Delta meet in products that matter; where one channel has an outlying query and
+ * another an outlying scale, logits lose bits that fp32 would keep (query x 20 in one channel, scale
+ * x 400 in another, d = 128: 5e-4 of a logit of about 100).
  * causal != 0: the stores' last n_tokens keys are the tokens' own, token t sees
  * the keys below n - n_tokens + 1 + t.  causal == 0: every token sees all n keys.
  *   K, V      stores with the same n, Hkv, d, n < 2^31 - 8192; each device- or

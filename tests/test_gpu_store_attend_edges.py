@@ -1,7 +1,8 @@
 """Attention over stores (fathom_store_attend, _batched, _partial) at its edges: a query that is not a number, short rows on
-both sides of what the device holds of clusters."""
+both sides of what the device holds of clusters, channels of very different magnitudes."""
 import math
 
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -11,7 +12,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 from bit_plane_key_b200 import fathom as F  # noqa: E402
-from test_gpu_store_attend import check, make_store, queries, reference  # noqa: E402
+from test_gpu_store_attend import check, make_store, queries, reference, values  # noqa: E402
 
 DEV = torch.device("cuda:0")
 
@@ -90,3 +91,51 @@ def test_no_short_row_waits_for_a_second_turn(d, G, n, few, many):
         calls.append(lambda ks=ks, vs=vs, q=q, out=out, ws=ws: F.store_attend(ks, vs, q, out=out, workspace=ws))
     a, b = _fastest(calls)
     assert b < 1.4 * a, (a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scales,mults", [({5: 100.0}, {}), ({7: 400.0}, {3: 20.0}), ({9: 2000.0}, {9: 1e-3, 11: 20.0}), ({}, {1: 1e4})])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+def test_a_logit_is_as_exact_as_stated(d, scales, mults, dtype):
+    """Stores of one key: a row's partial is its logit, s log2(e) = m + log2 l.  Off by at most, per channel, 2^-21 of the
+    factor q Delta and 2^-24 of the largest |q| times the largest Delta, under a code offset of 7.5; by (d/16 + 6) steps of
+    2^-23 of 15 sum |q Delta| in sums and scaling; and by 2^-20 in m + log2 l (l: 2^-22 by exp2 and the halves of the weight)."""
+    Hkv, G, T = 8, 8, 4
+    g = torch.Generator(device=DEV).manual_seed(d)
+    q = torch.randn(T, Hkv * G, d, device=DEV, generator=g)
+    x = torch.randn(Hkv, 1, d, device=DEV, generator=g)
+    for c, f in scales.items():
+        x[..., c] *= f
+    for c, f in mults.items():
+        q[..., c] *= f
+    q = q.to(dtype)
+    ks = F.Store.empty(Hkv, d, 1, device=DEV)
+    F.append_keys(ks, x, 1)
+    parts = F.store_attend_partial(ks, ks, q, 1).double().cpu().numpy()
+    got = (parts[..., d] + np.log2(parts[..., d + 1])) * math.log(2)
+    K, Kd = values(ks)
+    qn = q.double().cpu().numpy()
+    for t in range(T):
+        for h in range(Hkv * G):
+            f = np.abs(qn[t, h] * Kd[h // G, 0])
+            tol = 7.5 * (2.0 ** -21 * f.sum() + d * 2.0 ** -24 * np.abs(qn[t, h]).max() * Kd[h // G, 0].max())
+            tol = (tol + (d / 16 + 6) * 2.0 ** -23 * 15 * f.sum()) / math.sqrt(d) + 2.0 ** -20
+            s = K[h // G, 0] @ qn[t, h] / math.sqrt(d)
+            assert abs(got[t, h] - s) <= tol, (t, h, got[t, h] - s, tol)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scales,mults", [({5: 100.0}, {}), ({7: 400.0}, {3: 20.0}), ({9: 2000.0}, {9: 1e-3, 11: 20.0})])
+def test_outlying_channels(scales, mults, dtype):
+    n, Hkv, G, d = 700, 2, 4, 128
+    g = torch.Generator(device=DEV).manual_seed(7)
+    q, x = torch.randn(1, Hkv * G, d, device=DEV, generator=g), torch.randn(Hkv, n, d, device=DEV, generator=g)
+    for c, f in scales.items():
+        x[..., c] *= f
+    for c, f in mults.items():
+        q[..., c] *= f
+    q = q.to(dtype)
+    ks, vs = F.Store.empty(Hkv, d, n, device=DEV), make_store(n, Hkv, d, 2)
+    F.append_keys(ks, x, n)
+    ref, tol, _, _ = reference(ks, vs, q, n)
+    check(F.store_attend(ks, vs, q), ref, tol)
