@@ -49,10 +49,15 @@ struct CtxCache {
 // exit, instead of after that whole grid has completed; every kernel of the
 // path calls pdl_wait() before its first access to global memory (it returns
 // once the kernel before has completed and its writes are visible, at once
-// for a launch without the attribute).  The kernels release their dependents
-// only by exiting: an early release (griddepcontrol.launch_dependents at a
-// kernel's start) let the next grid's CTAs take SM space during the scan and
-// made the n = 131072 decode step slower (114 against 109 us on B200).
+// for a launch without the attribute).  The kernels of the decode step release
+// their dependents only by exiting: an early release
+// (griddepcontrol.launch_dependents at a kernel's start) let the next grid's CTAs
+// take SM space during the scan and made the n = 131072 decode step slower (114
+// against 109 us on B200).  store_attend_kernel alone releases at its start, with
+// its whole grid resident: the merge behind it, or the next call's kernel, is
+// scheduled as its CTAs leave.  That is safe behind any of them since all their
+// threads, those of CTAs without work too, wait before they read, write or leave,
+// so that a kernel is not over before the one ahead of it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // cudaLaunchKernelEx with the programmatic-serialization attribute when pdl,

@@ -305,7 +305,8 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
         copy_scales(s_rs + Sh::kRawScales, &map.vs[r.s], b, r.g * D, s_full + kRing);
     };
     Row rw = row_of(map.at, ub, Hkv, sets);
-    // the merge may be scheduled as this grid's CTAs leave (they are all resident from the start)
+    // the merge, or the next call's kernel, may be scheduled as this grid's CTAs leave (they are all resident from
+    // the start, clusters too)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (wp == kWarps - 1) {                             // the first queries go to other warps
         if (lane <= kRing) {

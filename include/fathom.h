@@ -482,7 +482,7 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
  *             largest times the largest scale below 2^112 (a NaN makes its head's output
  *             NaN, or 0 where the token sees no key, and no other's); 1 <= n_tokens <= 4096 (made
  *             for few tokens: the stores are read again for every 8 (token, head of a
- *             group) pairs).
+ *             group) pairs, in short calls for every 4).
  *   out       device, f32 [n_tokens][Hq][d].
  *   workspace device, 256-byte aligned, fathom_store_attend_workspace_bytes() bytes;
  *             contents need not be initialised, and are free once the call's
@@ -496,7 +496,7 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
  * Errors: EINVAL for null pointers, bad sizes, stores that differ, arrays not on
  * this device or not where host_resident says; ENOMEM for a short workspace;
  * EUNSUPPORTED for d other than 32, 64, 128, 256, and for more work than 2^26
- * tiles of 1024 keys for 8 pairs each.
+ * tiles of 1024 keys for up to 8 pairs each.
  */
 size_t fathom_store_attend_workspace_bytes(int n_sessions, int n_tokens, int n_q_heads, int n_kv_heads, int d);
 int fathom_store_attend(const fathom_store* K, const fathom_store* V, const void* q, int q_dtype, int n_tokens,
