@@ -734,7 +734,7 @@ store_attend_kernel(const __grid_constant__ Sessions<NS> map, const void* __rest
                 parts[h * (D + 2) + c] = o;
                 if (c == 0) parts[h * (D + 2) + D] = M, parts[h * (D + 2) + D + 1] = L;
             } else {
-                out[h * D + c] = L == 0.0f ? 0.0f : o / L;   // no key: 0; a sum that is no number shows
+                out[h * D + c] = o / (L > 0.0f ? L : 1.0f);   // no key: o is 0; a query with a NaN: o is one
             }
         };
         for (int e = threadIdx.x; e < kPairs * D; e += kThreads) {
@@ -889,7 +889,7 @@ store_attend_merge_kernel(const __grid_constant__ Spans<kAttendSets> map, const 
         if (c4 == 0) parts[h * (D + 2) + D] = M, parts[h * (D + 2) + D + 1] = L;
     } else {
         float* dst = out + h * D + 4 * c4;
-        const float r = L == 0.0f ? 1.0f : L;    // no key: o is 0
+        const float r = L > 0.0f ? L : 1.0f;     // as in the attention kernel
         dst[0] = o.x / r, dst[1] = o.y / r, dst[2] = o.z / r, dst[3] = o.w / r;
     }
 }
