@@ -980,18 +980,21 @@ int lay_out(Call& a, int tile, int granule) {
     return (int)U;
 }
 
-// Clusters of 2, 4 or 8 CTAs of the half tiles' kernel that the current device holds at once (an SM group's
-// last SMs may not make a whole one: B200, two CTAs to an SM: 148, 71, 33; one: 74, 33, 15); a device is asked once.
+// Clusters of 2, 4 or 8 CTAs of the half tiles' kernel that the current device holds at once, or (alone) holds with an
+// SM for each CTA.  A GPU's groups of SMs need not be whole clusters: on B200 it is 148, 71 and 33 at two CTAs to an
+// SM, and 74, 33 and 15 at one.  A device is asked once.
 template <int D, int NT, bool F32>
-int resident_clusters(int cluster) {
+int resident_clusters(int cluster, bool alone) {
     constexpr int kDevices = 64;
-    static std::atomic<int> known[kDevices][kMaxCluster + 1];   // the number and 1
+    static std::atomic<int> known[2][kDevices][kMaxCluster + 1];   // the number and 1
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
-    std::atomic<int>& at = known[dev][cluster];
+    std::atomic<int>& at = known[alone][dev][cluster];
     int held = at.load(std::memory_order_relaxed) - 1;
     if (held < 0) {
-        using Sh = Shape<D, NT, F32, 1>;
+        constexpr size_t kHalf = kMaxSmem / 2 + 1024;   // an SM has no room for two of these
+        constexpr size_t kSmem = Shape<D, NT, F32, 1>::kSmem;
+        const size_t smem = alone && kSmem < kHalf ? kHalf : kSmem;
         auto kern = store_attend_kernel<D, NT, F32, 1, 1>;
         cudaLaunchAttribute size;
         size.id = cudaLaunchAttributeClusterDimension;
@@ -1000,10 +1003,10 @@ int resident_clusters(int cluster) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(cluster);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Sh::kSmem;
+        cfg.dynamicSmemBytes = smem;
         cfg.attrs = &size;
         cfg.numAttrs = 1;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem) != cudaSuccess ||
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmem > kHalf ? kSmem : kHalf)) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&held, kern, &cfg) != cudaSuccess) {
             cudaGetLastError();
             return 0;
@@ -1014,19 +1017,19 @@ int resident_clusters(int cluster) {
 }
 
 // CTAs of the cluster that takes a row of 2 to 8 half tiles and adds its partials itself, or 1: each tile by itself
-// and a second launch, which costs 1.2 us.  Clusters that are not all resident take a second turn (1 query a head,
-// 2049 keys, 40 heads of 128: 18.2 us against 11.9; 16 heads of 256: 25.4 against 14.1).  Some 64 CTAs in clusters
-// of 4 and 8 lie two to an SM, which heads of 128 feel: there the second launch is shorter as long as it leaves an SM
-// to each tile (4096 keys, 8 heads: 8.5 us against 9.1; 12: 10.1 against 9.2; 16: 10.2 against 9.8; 20: 10.5 against
-// 11.8; heads of 64: 5.8 against 6.8, 6.7 against 6.9, 6.8 against 7.7, 7.0 against 8.6).
+// and a second launch, which costs 0.5 to 1.2 us.  Clusters that are not all resident take a second turn (2049 keys,
+// 40 heads of 128: 18.2 us against 11.9; 16 heads of 256: 25.4 against 14.1).  With heads of 128 two of a cluster's CTAs
+// on an SM cost more than the second launch where that would leave an SM to each tile (4096 keys, between two small
+// kernels and with them: 12 heads 11.3 us against 11.9, 16 heads 13.1 against 12.4, 20 heads, 160 tiles, 13.8 against
+// 14.2); with narrower heads they do not (16 heads of 32 8.2 against 9.1, 24 of 64, 1500 keys, 8 queries: 10.0 against 11.2).
 template <int D, int NT, bool F32>
 int cluster_of(const Call& a) {
     const int tiles = a.tiles(0, Shape<D, NT, F32, 1>::kTile), rows = a.Hkv * a.sets;
     if (tiles < 2 || tiles > kMaxCluster) return 1;
     int cluster = 2;
     while (cluster < tiles) cluster *= 2;
-    if (D == 128 && cluster > 2 && (int64_t)rows * cluster > 64 && (int64_t)rows * tiles <= 148) return 1;
-    return rows <= resident_clusters<D, NT, F32>(cluster) ? cluster : 1;
+    if (D >= 128 && (int64_t)rows * tiles <= 148 && rows > resident_clusters<D, NT, F32>(cluster, true)) return 1;
+    return rows <= resident_clusters<D, NT, F32>(cluster, false) ? cluster : 1;
 }
 
 template <int D, int NT, bool F32, int NS, int NB>
