@@ -139,3 +139,41 @@ def test_outlying_channels(scales, mults, dtype):
     F.append_keys(ks, x, n)
     ref, tol, _, _ = reference(ks, vs, q, n)
     check(F.store_attend(ks, vs, q), ref, tol)
+
+
+def test_a_first_call_may_be_a_captured_one():
+    """A process whose first attention over stores, a cluster's, a merged and a batched one, is captured: the device is asked
+    what it holds while the stream captures."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.path[:0] = %r
+import torch
+from bit_plane_key_b200 import fathom as F
+sets = []
+for n in (2500, 60000):
+    x = torch.randn(2, n, 128, device="cuda")
+    ks = F.Store.empty(2, 128, n, device="cuda")
+    F.append_keys(ks, x, n)
+    q = torch.randn(8, 128, device="cuda")
+    sets.append((ks, q, torch.empty(8, 128, device="cuda"), torch.empty(F.store_attend_workspace_bytes(ks, 2, 1, 8), dtype=torch.uint8, device="cuda")))
+both = torch.empty(2, 1, 8, 128, device="cuda")
+two = torch.stack([s[1] for s in sets])[:, None].contiguous()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for ks, q, out, ws in sets:
+        F.store_attend(ks, ks, q, out=out, workspace=ws)
+    F.store_attend_batched([s[0] for s in sets], [s[0] for s in sets], two, out=both, workspace=sets[0][3])
+g.replay()
+torch.cuda.synchronize()
+for i, (ks, q, out, ws) in enumerate(sets):
+    assert torch.equal(out, F.store_attend(ks, ks, q))
+    assert ((both[i, 0] - out).norm() <= 1e-5 * out.norm()).item()
+assert F.last_device_status() == 0
+print("replayed")
+""" % ([os.path.dirname(os.path.dirname(os.path.abspath(__file__)))],)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stderr[-2000:]
