@@ -40,14 +40,15 @@
 // multiples of a power of two that is large enough for their sums to be exact, as
 // the offset is; what is cut off the low halves' sums is 2^-10 smaller.  The running
 // maximum is rounded up to a whole number of binary orders: what was summed
-// is rescaled exactly.  Against 64 bits: 2e-7 to 7e-7 of the output (fp32 arithmetic: 2e-7
-// to 2.6e-6).  The halves are fixed point: their last place is that of the head's largest |q|
+// is rescaled exactly.  Against 64 bits: 2e-7 to 1e-6 of the output (fp32 arithmetic: 2e-7
+// to 4e-6; 4096 keys 2.4e-7 against 1.8e-7, 131072 4.5e-7 against 1.9e-6).  The
+// halves are fixed point: their last place is that of the head's largest |q|
 // times the block's largest Delta (2^-24 of it), so where those two do not meet in one
 // channel, logits lose bits that fp32 would keep.
 //
 // What bounds it: the instructions around the products, ALU and issue slots, not the
 // memory: 0.27 us per 64-key block and SM where the copies alone take 0.20; and
-// 13 us of launches, first copies and merge.  1048576 keys (4 heads of 128, 4 queries
+// 13 us of launches, first copies and merge.  1048576 keys (8 heads of 128, 4 queries
 // each): 264 us, 4.3 TB/s; 131072: 46 us; 4096 keys of 1 head: 8.0 us.
 #include <cuda.h>
 

@@ -470,7 +470,7 @@ int fathom_append_rows(fathom_store* K, fathom_store* V, const uint16_t* K_rows,
  * The products run on the matrix units, their operands in two fp16 halves: a factor
  * q_c Delta_c is off by at most 2^-21 of itself plus 2^-24 of the largest |q| of the head times
  * the largest Delta of the block, a weight by 2^-23 of the block's largest weight (or 2^-35 of all).
- * That is at or below what fp32 arithmetic loses as long as a head's largest |q|
+ * That is about what fp32 arithmetic loses, and less over many keys, as long as a head's largest |q|
  * and the largest Delta meet in products that matter; where one channel has an outlying query and
  * another an outlying scale, logits lose bits that fp32 would keep (query x 20 in one channel, scale
  * x 400 in another, d = 128: 5e-4 of a logit of about 100).
